@@ -336,7 +336,8 @@ def _handles(s):
             ws = ad.kv8_attention_workspace(B, Hq, Hkv, s["cap"], weights=case["weights"])
             s["calls"] = [ad.PreparedKV8Attention(s["q"], kv, s["lens"], ws, s["out"], **more)]
         else:
-            ws = ad.kv8_sparse_attention_workspace(B, Hq, Hkv, case["k"], weights=case["weights"])
+            ws = ad.kv8_sparse_attention_workspace(B, Hq, Hkv, case["k"], shared=case["shared"],
+                                                   weights=case["weights"])
             s["calls"] = [ad.PreparedKV8SparseAttention(s["q"], kv, s["idx"], ws, s["out"],
                                                         shared=case["shared"], **more)]
 
