@@ -463,6 +463,177 @@ adamas_status adamas_decode_plan_shared(int B, int Hq, int Hkv, int d, int64_t L
                                         int* ctas, int* cluster, int64_t* tokens_per_cta,
                                         int* smem_bytes);
 
+/* ------------------------------------------------------------------------------
+ * Caches held in 8 bits.  The pages keep the original K/V states in 16 bits and do
+ * not treat compressed caches; these entry points are the implementation's: they
+ * hold, read, attend over and shorten a cache whose K and V rows take one byte per
+ * value (half the bytes of bf16), beside the same 2-bit key codes.
+ *
+ * Format.  A block is block_size consecutive positions of one (batch, kv head); K
+ * and V have one float32 scale S per block, and a stored byte v (e4m3, or int8 in
+ * -127..127) stands for v * S.  adamas_kv8_append and adamas_kv8_evict write scales
+ * that are powers of two: S(a) = 2^E with the smallest E >= -126 for which the block's
+ * largest finite magnitude a satisfies a <= 448 S (e4m3) or a <= 127 S (int8), and
+ * bytes rounded to nearest, ties to even.  Division by S is then exact, so a byte
+ * does not depend on how the division was rounded, and e4m3 rows moved to a larger
+ * scale lose bits only below the smallest normal value.  The readers (adamas_kv8_read
+ * and both attentions) take any finite S >= 0.  An e4m3 NaN stays NaN; an infinity is
+ * stored as the largest value; int8 stores NaN as 0.
+ *
+ * Contiguous caches (page_size = 0): k, v [B][Hkv][Lmax][d] bytes, k_scale, v_scale
+ * [B][Hkv][Lmax / block_size], codes [B][Hkv][Lmax][d/4].  Paged caches (page_size > 0,
+ * a power of two in [block_size, 2^20]): k, v [num_pages][Hkv][page_size][d],
+ * scales [num_pages][Hkv][page_size / block_size], codes
+ * [num_pages][Hkv][page_size][d/4]; position p of sequence b is row p % page_size of
+ * page block_table[b * max_blocks_per_seq + p / page_size], and Lmax is the longest
+ * sequence (Lmax <= max_blocks_per_seq * page_size).  block_size is a power of two in
+ * [1, 256]; contiguous caches need Lmax % block_size == 0.  A page that is written
+ * (append, evict) must belong to one sequence.  codes may be NULL.  Alignment: 16
+ * bytes for rows and codes, 4 for scales and integer arrays, 256 for workspaces.
+ *
+ * Errors met on the device (a length, position or page id out of range) are recorded
+ * in the workspace's error word (adamas_check_workspace returns
+ * ADAMAS_ERR_INVALID_ARG); the row concerned is left out of the operation.
+ * ------------------------------------------------------------------------------ */
+typedef enum { ADAMAS_KV8_E4M3 = 0, ADAMAS_KV8_INT8 = 1 } adamas_kv8_format;
+
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  uint8_t* codes;               /* NULL: no key codes are kept */
+  const int32_t* block_table;   /* [B][max_blocks_per_seq]; NULL when page_size = 0 */
+  int64_t Lmax;
+  int64_t num_pages;
+  int32_t format;               /* adamas_kv8_format */
+  int32_t block_size;
+  int32_t B;
+  int32_t Hkv;
+  int32_t d;                    /* 128 */
+  int32_t page_size;            /* 0: contiguous */
+  int32_t max_blocks_per_seq;
+  int32_t reserved;             /* 0 */
+} adamas_kv8_cache;
+
+/*
+ * Appends rows to an 8-bit cache.  Sequence b's counts[b] new rows (counts NULL: n_new
+ * each; 0 <= counts[b] <= n_new) go to positions [starts[b], starts[b] + counts[b]);
+ * starts and counts are device int32 arrays [B].  k_new and v_new hold elements of
+ * `dt`; row i of (b, h) starts at element b * stride_b + h * stride_h + i * stride_n
+ * (the same strides for both, multiples of 16 bytes, >= 0), its d elements contiguous.
+ * A touched block's scale is S(largest magnitude of its new rows); if the block also
+ * holds positions below starts[b], it is at least the block's present scale, and
+ * those rows are rounded once more when the scale grows.  Rows of the block at and
+ * after starts[b] + counts[b] keep their bytes.  With cache->codes the new keys' codes
+ * are written too, from the rows as given: ratio = 0 uses the fixed threshold t,
+ * 0 < ratio <= 1 per-vector thresholds (adamas_encode_keys_absmax).  A sequence whose
+ * start or count is out of range is left alone.  ws: at least 256 bytes.
+ */
+adamas_status adamas_kv8_append(const adamas_kv8_cache* cache, const void* k_new,
+                                const void* v_new, adamas_dtype dt, int64_t n_new,
+                                int64_t stride_b, int64_t stride_h, int64_t stride_n,
+                                const int32_t* starts, const int32_t* counts, float t,
+                                float ratio, void* workspace, size_t ws_bytes,
+                                cudaStream_t stream);
+
+/*
+ * Values of the n positions from starts[b] (device int32 [B]) of every sequence and kv
+ * head: k_out, v_out [B][Hkv][n][d] elements of out_dt, v * S rounded to out_dt (bf16:
+ * exact for power-of-two scales).  Positions outside [0, Lmax) give zeros.
+ */
+adamas_status adamas_kv8_read(const adamas_kv8_cache* cache, const int32_t* starts, int64_t n,
+                              adamas_dtype out_dt, void* k_out, void* v_out, void* workspace,
+                              size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Dense attention of one query token per sequence over an 8-bit cache: for query head
+ * h of kv head h / G, softmax over the positions j < seq_lens[b] of
+ * (q . K_j) / sqrt(d), fp32 accumulation, out [B][Hq][d] float32.  seq_lens: device
+ * int32 [B], each in [0, Lmax] (others are clamped and recorded); NULL: Lmax each.  A
+ * sequence of length 0 gives zeros.  Any G = Hq / Hkv from 1 to 8.
+ *
+ * With weights_out (device float32 [B][Hkv][Lmax]) every position's attention weight,
+ * summed over the G query heads of its kv head, is added to weights_in:
+ * weights_out[b][kv][j] = weights_in[b][kv][j] + sum_g p_g(j) for j < seq_lens[b]; other
+ * entries are not written.  weights_in may equal weights_out (a running sum) and is
+ * required with it.
+ *
+ * The workspace (adamas_kv8_attention_workspace_bytes, weights 0 or 1) is zero-filled
+ * once (adamas_workspace_init); each call leaves its counters at zero.  Calls that may
+ * run at the same time need one workspace each.
+ */
+size_t adamas_kv8_attention_workspace_bytes(int B, int Hq, int Hkv, int d, int64_t Lmax,
+                                            int weights);
+adamas_status adamas_kv8_attention(const void* q, adamas_dtype dt, const adamas_kv8_cache* cache,
+                                   int Hq, const int32_t* seq_lens, void* workspace,
+                                   size_t ws_bytes, const float* weights_in, float* weights_out,
+                                   float* out, cudaStream_t stream);
+
+/*
+ * Attention over selected positions of an 8-bit cache (adamas_sparse_attention's
+ * counterpart): idx [B][Hq][k], or [B][Hkv][k] with shared = 1 (one list for the G
+ * heads of a kv head), as adamas_select_topk / _shared / _paged write them, in any order.
+ * Entries below 0 are skipped (a list of only such entries gives zeros); an entry at or
+ * above Lmax is skipped and recorded; a position given twice counts twice.
+ * weights_in / weights_out as in adamas_kv8_attention, except that every entry j < Lmax
+ * is written when the two differ (weights_in plus what was attended); sums are
+ * formed head by head, so they are reproducible when no list repeats a position.
+ */
+size_t adamas_kv8_sparse_attention_workspace_bytes(int B, int Hq, int Hkv, int d, int k,
+                                                   int shared, int weights);
+adamas_status adamas_kv8_sparse_attention(const void* q, adamas_dtype dt,
+                                          const adamas_kv8_cache* cache, int Hq,
+                                          const int32_t* idx, int k, int shared,
+                                          void* workspace, size_t ws_bytes,
+                                          const float* weights_in, float* weights_out,
+                                          float* out, cudaStream_t stream);
+
+/*
+ * Which positions stay when a cache is cut to `budget` rows per kv head, by accumulated
+ * attention weight.  n = min(seq_lens[b], budget) positions stay: all of them if
+ * seq_lens[b] <= budget, else the first `sink`, the last `recent` (sink + recent <=
+ * budget) and the budget - sink - recent positions between with the largest weights
+ * (float32 [B][Hkv][Lmax]; NaN counts as -inf), ties going to the lower position.
+ * keep [B][Hkv][budget] int32 receives them ascending, then -1.  weights_out (nullable,
+ * [B][Hkv][Lmax_out], Lmax_out >= budget; may equal weights when Lmax_out = Lmax)
+ * receives the kept weights at 0 .. n - 1 and zeros at n .. min(seq_lens[b], Lmax_out) - 1.
+ * Lmax at most 786432 (ADAMAS_ERR_UNSUPPORTED above).
+ */
+adamas_status adamas_evict_select(const float* weights, int B, int Hkv, int64_t Lmax,
+                                  const int32_t* seq_lens, int budget, int sink, int recent,
+                                  int32_t* keep, float* weights_out, int64_t Lmax_out,
+                                  void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Moves kept rows together: row i of (b, kv head) of dst becomes row keep[b][h][i] of src
+ * for i < min(seq_lens[b], n_keep); other rows of dst are left as they are.  Rows of
+ * row_bytes (32, 256 or 512: codes, bf16 or fp32 rows) in the cache layouts of
+ * adamas_decode_step (page_size = 0) or adamas_decode_step_paged.  dst may equal src
+ * (the move is then done in place; keep must be ascending); otherwise they must not
+ * overlap.  keep as written by adamas_evict_select for the same seq_lens.
+ */
+adamas_status adamas_compact_rows(const void* src, void* dst, int row_bytes, int B, int Hkv,
+                                  int64_t Lmax, int page_size, int64_t num_pages,
+                                  const int32_t* block_table, int max_blocks_per_seq,
+                                  const int32_t* keep, int n_keep, const int32_t* seq_lens,
+                                  void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Eviction from an 8-bit cache: adamas_evict_select, then the kept rows of `src` move to
+ * positions 0 .. n - 1 of `dst` (K, V, and codes when dst->codes is given), requantised
+ * block by block: S(largest magnitude of the block's kept values), bytes rounded from
+ * the kept values.  A block in place whose rows all stay where they are keeps bytes and
+ * scale.  lens_out[b] = min(seq_lens[b], budget) (lens_out may equal seq_lens).  dst may be
+ * the same cache (in place) or one that shares no memory with src, of the same format,
+ * B and Hkv, with dst->Lmax >= budget.  weights_out is [B][Hkv][dst->Lmax].
+ */
+adamas_status adamas_kv8_evict(const adamas_kv8_cache* src, const adamas_kv8_cache* dst,
+                               const float* weights_in, float* weights_out,
+                               const int32_t* seq_lens, int32_t* lens_out, int budget, int sink,
+                               int recent, int32_t* keep, void* workspace, size_t ws_bytes,
+                               cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -105,6 +105,22 @@ _SIGNATURES = {
     "adamas_decode_plan_shared": (_c_i, [_c_i, _c_i, _c_i, _c_i, _c_i64, _c_i,
                                          ctypes.POINTER(_c_i), ctypes.POINTER(_c_i),
                                          ctypes.POINTER(_c_i64), ctypes.POINTER(_c_i)]),
+    "adamas_kv8_append": (_c_i, [_c_p, _c_p, _c_p, _c_i, _c_i64, _c_i64, _c_i64, _c_i64, _c_p,
+                                 _c_p, _c_f, _c_f, _c_p, _c_sz, _c_p]),
+    "adamas_kv8_read": (_c_i, [_c_p, _c_p, _c_i64, _c_i, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "adamas_kv8_attention_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i, _c_i, _c_i64, _c_i]),
+    "adamas_kv8_attention": (_c_i, [_c_p, _c_i, _c_p, _c_i, _c_p, _c_p, _c_sz, _c_p, _c_p, _c_p,
+                                    _c_p]),
+    "adamas_kv8_sparse_attention_workspace_bytes": (_c_sz, [_c_i, _c_i, _c_i, _c_i, _c_i, _c_i,
+                                                            _c_i]),
+    "adamas_kv8_sparse_attention": (_c_i, [_c_p, _c_i, _c_p, _c_i, _c_p, _c_i, _c_i, _c_p, _c_sz,
+                                           _c_p, _c_p, _c_p, _c_p]),
+    "adamas_evict_select": (_c_i, [_c_p, _c_i, _c_i, _c_i64, _c_p, _c_i, _c_i, _c_i, _c_p, _c_p,
+                                   _c_i64, _c_p, _c_sz, _c_p]),
+    "adamas_compact_rows": (_c_i, [_c_p, _c_p, _c_i, _c_i, _c_i, _c_i64, _c_i, _c_i64, _c_p, _c_i,
+                                   _c_p, _c_i, _c_p, _c_p, _c_sz, _c_p]),
+    "adamas_kv8_evict": (_c_i, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, _c_p, _c_p,
+                                _c_sz, _c_p]),
 }
 
 
@@ -667,8 +683,19 @@ def sparse_attention_noalloc(q, k_cache, v_cache, idx, out=None, stream=None):
     return out
 
 
+# caches held in 8 bits (imports the binding above)
+from token_level_sparse_fwht_b200.kv8 import (  # noqa: E402
+    KV8Cache, PreparedKV8Append, PreparedKV8Attention, PreparedKV8Evict, PreparedKV8Read,
+    PreparedKV8SparseAttention, compact_rows, evict_select, kv8_append, kv8_attention,
+    kv8_attention_workspace, kv8_cache, kv8_evict, kv8_read, kv8_sparse_attention,
+    kv8_sparse_attention_workspace, kv8_workspace)
+
 __all__ = ["lib", "header_symbols", "status_string", "AdamasError", "encode_keys",
            "decode_step_host", "PreparedDecodeHost",
            "encode_queries", "decode_workspace_bytes", "decode_plan", "init_workspace",
            "decode_workspace", "check_workspace", "decode_step", "select_topk",
-           "sparse_attention_workspace", "sparse_attention", "sparse_attention_noalloc"]
+           "sparse_attention_workspace", "sparse_attention", "sparse_attention_noalloc",
+           "KV8Cache", "kv8_cache", "kv8_workspace", "kv8_append", "kv8_read", "kv8_attention",
+           "kv8_attention_workspace", "kv8_sparse_attention", "kv8_sparse_attention_workspace",
+           "kv8_evict", "evict_select", "compact_rows", "PreparedKV8Append", "PreparedKV8Read",
+           "PreparedKV8Attention", "PreparedKV8SparseAttention", "PreparedKV8Evict"]
