@@ -22,45 +22,48 @@
 // B fragment it needs for the values, so nothing is exchanged between the products.  The
 // order of dimensions inside a product is free: a lane takes 16 contiguous bytes of a K
 // row per load, and 16 contiguous dimensions of a V row (its outputs), pairs of keys
-// interleaved by byte permutes.  With G <= 4 the 8 columns hold the high and the low parts of w
-// for four heads (head rows repeated); with G <= 8 there are two column tiles.
+// interleaved by byte permutes.  With G <= 4 (NT = 1) the 8 columns hold the high and the low
+// parts of w for four heads (head rows repeated); with G <= 8 (NT = 2) each product is taken
+// twice, with the high and with the low parts.
 //
-// Layout of the work.  A step is 128 keys of a unit: 16 per warp, 8 warps.  The steps of all
+// Layout of the work.  A step is 256 keys of a unit: 32 per warp, 8 warps.  The steps of all
 // units form one line that is cut evenly over the CTAs (lengths are read on the device),
 // so unequal sequences balance; a CTA's cut may hold the end of one unit, whole units and
-// the start of another.  Each warp streams its own keys through a ring of kStages tiles in
-// shared memory (16-byte asynchronous copies, rows swizzled in 16-byte chunks so that both
-// products read without bank conflicts), the copies running ahead over unit borders.
-// At a unit's end the 8 warps' states are merged; a unit cut between CTAs is merged from the
-// partial results in the workspace, in CTA order, by the last CTA to finish its part.
+// the start of another.  Each lane loads the 16-byte pieces of K and V rows that its fragments
+// need straight into registers: a tile's K registers are refilled (with the next tile, of the next
+// unit if need be) as soon as its scores are formed, the V registers after its value product,
+// so 8 KB per warp stay under way through the rest of the work.  At a unit's end the warps'
+// states are merged; a unit cut between CTAs is merged from the partial results in the workspace,
+// in CTA order, by the last CTA to finish its part.
+//
+// kUni: 16 rows of a tile follow one another and share one scale (contiguous caches and pages
+// of at least 16 rows, blocks of at least 16 positions); otherwise (given positions, small
+// pages or blocks) rows and scales are looked up key by key.
+#include <type_traits>
+
 #include "kv8_internal.cuh"
 
 namespace adamas {
 
 namespace {
 
-constexpr int kAtWarps = 8;
-constexpr int kAtThreads = kAtWarps * 32;
-constexpr int kTile = 16;                        // keys per warp and step
-constexpr int kStep = kAtWarps * kTile;          // keys per step
-constexpr int kTileBytes = 2 * kTile * kD;       // K rows, then V rows
+constexpr int kWarps = 8;                        // one CTA per SM: up to 255 registers a thread
+constexpr int kThr = kWarps * 32;
+constexpr int kTile = 32;                        // keys per warp and step, in two halves of 16
+constexpr int kStep = kWarps * kTile;            // keys per step
+constexpr int kMaxParts = 160;                   // parts of a unit whose factors fit in shared memory
 constexpr float kWBias = 14.0f;                  // w is held times 2^14
 constexpr int kPart = 4 + kD;                    // floats of a partial: m, l, m2, 0, sums
 
 // Shared memory of a CTA.
-template <int NT, int ST>
+template <int NT>
 struct Smem {
   static constexpr int kSums = NT == 1 ? 16 : 32;   // values per lane when warps are merged
-  uint8_t ring[kAtWarps][ST][kTileBytes];
-  float scale[kAtWarps][ST][2 * kTile];             // K scales, then V scales
-  float sums[kAtWarps / 2][kSums][32];              // merge of the warps; combine scratch
-  float stat[kAtWarps][8][4];                       // m, l, m2 per warp and head
-  uint32_t mask[kAtWarps][ST];                      // which of a tile's keys exist
-  float fin[8][2];                                  // M2 and the output factor per head
-  long long base;                                   // steps before the first sequence
-  long long total;
-  int first_b;
-  int last;
+  float sums[kWarps][kSums][32];                    // merge of the warps; combine scratch
+  float stat[kWarps][8][4];                         // m, l, m2 per warp and head
+  float fin[8][4];                                  // per head: M, M2, 1 / l, output factor
+  float fac[kMaxParts][8];                          // combine: a part's factor per head
+  int last[2];
 };
 
 struct Args {
@@ -91,6 +94,16 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// the first product of a chain: no sum to add to
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -103,22 +116,17 @@ __device__ __forceinline__ float ref_change(float from, float to) {
   return from == to ? 1.0f : ex2(from - to);
 }
 
-// cp.async that fills with zeros when !ok (nothing is read then)
-__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(ok ? 16 : 0)
-               : "memory");
+// 16 bytes that are read once (kept out of L1); zeros if !ok (nothing is read then).
+__device__ __forceinline__ uint4 load_row16(const uint8_t* p, bool ok = true) {
+  uint4 v;
+  if (!ok)
+    v = make_uint4(0u, 0u, 0u, 0u);
+  else
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+  return v;
 }
-__device__ __forceinline__ void cp_async_4_or_zero(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-               "r"(ok ? 4 : 0)
-               : "memory");
-}
-
-// 16-byte chunk ch of row r of a tile is stored at chunk ch ^ swz(r): the 8 lanes of a
-// load phase (two K rows 2i, 2i + 1 and four neighbouring chunks; four V rows 2i or 2i + 1
-// and two neighbouring chunks) then cover all 32 banks.
-__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r & 1) << 2); }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
@@ -130,7 +138,7 @@ __device__ __forceinline__ uint32_t pack_f16_rest(float lo, float hi, uint32_t t
   return pack_f16(lo - t.x, hi - t.y);
 }
 
-// One step's place: unit u = (b, j), its step ls of ns.
+// One step's place: unit (b, j), its step ls of ns.
 struct Place {
   int b, j;
   int ls, ns;
@@ -156,42 +164,116 @@ __device__ __forceinline__ void next_place(const Args& a, Place& p) {
   } while (p.ns == 0);   // the caller only moves on while steps remain
 }
 
-// Row of key `n` (0 .. 15) of this warp's tile at place p, or -1.
-__device__ __forceinline__ int64_t key_row(const Args& a, const Place& p, int warp, int n) {
-  const int i = p.ls * kStep + warp * kTile + n;
-  if (i >= p.len) return -1;
-  int64_t pos = i;
-  const int h = p.j / a.heads_per_kv;
-  if (a.idx != nullptr) {
-    pos = a.idx[(int64_t(p.b) * a.U + p.j) * a.k + i];
-    if (pos < 0) return -1;
-    if (pos >= a.c.Lmax) {
-      atomicOr(a.err, kErrInput);
-      return -1;
-    }
+// This warp's tile at a place, found in three stages an iteration apart, because each may wait
+// for a load: the positions (given lists), the pages (block tables), the rows.
+struct Tile {
+  int b, j, i0, n;      // unit, first key, keys (0 .. 32)
+  int pos;              // lane i: key i's position
+  int page[2];          // kUni: of each half; else lane i: key i's, in [0]
+};
+// A cache has fewer than 2^31 rows, so a row index is an int.  kUni: the row of the first key of
+// each half, in every lane; else lane i holds key i's row.  mask: which of the keys are there.
+struct Rows {
+  int row[2];
+  uint32_t mask;
+};
+
+__device__ __forceinline__ Tile no_tile() { return Tile{0, 0, 0, 0, -1, {0, 0}}; }
+
+template <bool kUni>
+__device__ __forceinline__ Tile tile_positions(const Args& a, const Place& p, int warp, int lane) {
+  Tile t;
+  t.b = p.b;
+  t.j = p.j;
+  t.i0 = p.ls * kStep + warp * kTile;
+  t.n = max(0, min(kTile, p.len - t.i0));
+  t.pos = -1;
+  t.page[0] = t.page[1] = 0;
+  if constexpr (!kUni) {
+    if (lane < t.n)
+      t.pos = a.idx != nullptr ? a.idx[(int64_t(p.b) * a.U + p.j) * a.k + t.i0 + lane]
+                               : t.i0 + lane;
   }
-  const int64_t row = kv8_row(a.c, p.b, h, pos);
-  if (row < 0) atomicOr(a.err, kErrInput);
-  return row;
+  return t;
 }
 
-// The query rows of a unit as A fragments.  Lane (gid, q) holds head row gid: elements
-// 4 i .. 4 i + 3 of its 16-dimension runs (chunk c: dimensions 64 (c / 4) + 16 q +
-// 4 (c % 4) + 0..3), scaled by 2^-e so that the head's largest element lies in [1, 2) x 2^14;
-// the returned factor undoes it: x = dot * a_j * factor.
+template <bool kUni>
+__device__ __forceinline__ void tile_pages(const Args& a, Tile& t) {
+  if (a.c.table == nullptr) return;
+  const int32_t* const table = a.c.table + int64_t(t.b) * a.c.max_blocks;
+  if constexpr (kUni) {
+    if (t.n > 0) t.page[0] = table[t.i0 >> a.c.page_shift];
+    if (t.n > 16) t.page[1] = table[(t.i0 + 16) >> a.c.page_shift];
+  } else {
+    if (t.pos >= 0 && t.pos < a.c.Lmax) t.page[0] = table[t.pos >> a.c.page_shift];
+  }
+}
+
+template <bool kUni>
+__device__ __forceinline__ Rows tile_rows(const Args& a, const Tile& t) {
+  Rows r;
+  r.row[0] = r.row[1] = -1;
+  r.mask = t.n >= 32 ? 0xffffffffu : (1u << t.n) - 1u;
+  if constexpr (kUni) {
+    if (a.c.table == nullptr) {
+      r.row[0] = (t.b * a.c.Hkv + t.j) * int(a.c.Lmax) + t.i0;
+      r.row[1] = r.row[0] + 16;
+    } else {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (t.page[u] < 0 || t.page[u] >= a.c.num_pages) {
+          if (t.n > 16 * u) atomicOr(a.err, kErrInput);
+          r.mask &= u ? 0x0000ffffu : 0xffff0000u;
+        } else {
+          r.row[u] = ((t.page[u] * a.c.Hkv + t.j) << a.c.page_shift) +
+                     ((t.i0 + 16 * u) & ((1 << a.c.page_shift) - 1));
+        }
+      }
+    }
+  } else {
+    if (t.pos >= 0) {
+      const int h = t.j / a.heads_per_kv;
+      if (t.pos >= a.c.Lmax || t.page[0] < 0 || t.page[0] >= (a.c.table ? a.c.num_pages : 1))
+        atomicOr(a.err, kErrInput);
+      else if (a.c.table == nullptr)
+        r.row[0] = (t.b * a.c.Hkv + h) * int(a.c.Lmax) + t.pos;
+      else
+        r.row[0] = ((t.page[0] * a.c.Hkv + h) << a.c.page_shift) +
+                   (t.pos & ((1 << a.c.page_shift) - 1));
+    }
+    r.mask = __ballot_sync(0xffffffffu, r.row[0] >= 0);
+  }
+  return r;
+}
+
+// The query rows of a unit.  Lane (gid, q) holds head row gid: elements 4 i .. 4 i + 3 of its
+// 16-dimension runs (chunk c: dimensions 64 (c / 4) + 16 q + 4 (c % 4) + 0..3).
+template <typename T>
+struct QueryRow {
+  typename Raw4<T>::type raw[8];
+  __device__ __forceinline__ void load(const void* base, int64_t row, bool exists, int q) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      raw[c] = {};
+      if (exists)
+        raw[c] = Raw4<T>::load(static_cast<const T*>(base) + row * kD, 16 * (c >> 2) + 4 * q + (c & 3));
+    }
+  }
+};
+
+// The rows as A fragments, scaled by 2^-e so that the head's largest element lies in
+// [1, 2) x 2^14; the returned factor undoes it: x = dot * a_j * factor.
 template <typename T, bool kLo>
-__device__ __forceinline__ float load_q(const Args& a, int64_t row, bool exists, int q,
-                                        uint32_t (&hi)[8][2], uint32_t (&lo)[kLo ? 8 : 1][2]) {
-  float v[8][4];
+__device__ __forceinline__ float query_fragments(const QueryRow<T>& qr, float scale_log2,
+                                                 uint32_t (&hi)[8][2],
+                                                 uint32_t (&lo)[kLo ? 8 : 1][2]) {
   float mx = 0.0f;
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
+    float v[4];
+    Raw4<T>::decode(qr.raw[c], v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[c][i] = 0.0f;
-    if (exists)
-      load4(static_cast<const T*>(a.q) + row * kD, 16 * (c >> 2) + 4 * q + (c & 3), v[c]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(v[c][i]));
+    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(v[i]));
   }
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -201,320 +283,508 @@ __device__ __forceinline__ float load_q(const Args& a, int64_t row, bool exists,
   const float down = pow2i(14 - e);
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
+    float v[4];
+    Raw4<T>::decode(qr.raw[c], v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[c][i] *= down;
-    hi[c][0] = pack_f16(v[c][0], v[c][1]);
-    hi[c][1] = pack_f16(v[c][2], v[c][3]);
+    for (int i = 0; i < 4; ++i) v[i] *= down;
+    hi[c][0] = pack_f16(v[0], v[1]);
+    hi[c][1] = pack_f16(v[2], v[3]);
     if constexpr (kLo) {
-      lo[c][0] = pack_f16_rest(v[c][0], v[c][1], hi[c][0]);
-      lo[c][1] = pack_f16_rest(v[c][2], v[c][3], hi[c][1]);
+      lo[c][0] = pack_f16_rest(v[0], v[1], hi[c][0]);
+      lo[c][1] = pack_f16_rest(v[2], v[3], hi[c][1]);
     }
   }
-  return a.scale_log2 * pow2i(e - 14);
+  return scale_log2 * pow2i(e - 14);
 }
 
-// FMT: byte format; NT: column tiles of the value product (1: G <= 4, 2: G <= 8); kLo: fp32
-// queries; ST: ring stages.
-template <typename T, int FMT, int NT, int ST, int kMinBlocks>
-__global__ void __launch_bounds__(kAtThreads, kMinBlocks) kv8_attention_kernel(const Args a) {
-  constexpr bool kLo = sizeof(T) == 4;
-  using S = Smem<NT, ST>;
-  extern __shared__ __align__(128) uint8_t smem_raw[];
-  S& sm = *reinterpret_cast<S*>(smem_raw);
+// The even cut of T steps over C CTAs: the first T % C take one step more.
+struct Cut {
+  int q, r;
+  __device__ __forceinline__ int start(int c) const { return c * q + min(c, r); }
+  __device__ __forceinline__ int owner(int s) const {
+    const int wide = r * (q + 1);
+    return s < wide ? s / (q + 1) : r + (s - wide) / q;
+  }
+};
+
+// Merges a unit's parts (in CTA order) into its output: the references and sums of every
+// head first (a warp per head), which gives each part's factor, then the sums over the parts,
+// threads = (part group, head, 4 dimensions) with kBatch loads under way each.
+template <int NT>
+__device__ __forceinline__ void combine_parts(const Args& a, Smem<NT>& sm, const Cut& cut,
+                                              int64_t unit, int u0, int c0, int parts) {
+  constexpr int kBatch = 16;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int first = 2 * c0 + (cut.start(c0) < u0 ? 1 : 0);   // slot of part 0; then 2 (c0 + p)
+  const auto at = [&](int p, int h) {
+    return a.part + (int64_t(p == 0 ? first : 2 * (c0 + p)) * a.G + h) * kPart;
+  };
+  const int cols = a.G * (kD / 4);
+  const int groups = kThr / cols;
+  const int gr = tid / cols, ci = tid % cols;
+  const int hh = ci / (kD / 4), d4 = ci % (kD / 4);
+  float4 y[kBatch];
+  const auto load = [&](int p0) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int p = p0 + u * groups;
+      y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (gr < groups && p < parts) y[u] = __ldcg(reinterpret_cast<const float4*>(at(p, hh) + 4) + d4);
+    }
+  };
+  load(gr);   // under way while the factors are found
+  if (warp < a.G) {
+    float hM = -INFINITY, hM2 = -INFINITY;
+    float4 o[kMaxParts / 32];
+#pragma unroll
+    for (int i = 0; i < kMaxParts / 32; ++i) {
+      const int p = lane + 32 * i;
+      o[i] = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+      if (p < parts) o[i] = __ldcg(reinterpret_cast<const float4*>(at(p, warp)));
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxParts / 32; ++i) {
+      hM = fmaxf(hM, o[i].x);
+      hM2 = fmaxf(hM2, o[i].z);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      hM = fmaxf(hM, __shfl_xor_sync(0xffffffffu, hM, o));
+      hM2 = fmaxf(hM2, __shfl_xor_sync(0xffffffffu, hM2, o));
+    }
+    float hl = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMaxParts / 32; ++i) {
+      hl += o[i].y * ref_change(o[i].x, hM);
+      if (lane + 32 * i < parts) sm.fac[lane + 32 * i][warp] = ref_change(o[i].z, hM2);
+    }
+    hl = warp_sum(hl);
+    if (lane == 0) {
+      const bool some = hl > 0.0f || !(hl == hl);
+      sm.fin[warp][3] = some ? ex2(hM2 - hM - kWBias) / hl : 0.0f;
+      if (a.stats != nullptr) {
+        float* const o = a.stats + (unit * a.G + warp) * 2;
+        o[0] = some ? hM : 0.0f;
+        o[1] = some ? 1.0f / hl : 0.0f;
+      }
+    }
+  }
+  __syncthreads();
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (gr < groups) {
+    for (int p0 = gr; p0 < parts; p0 += kBatch * groups) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int p = p0 + u * groups;
+        if (p < parts) {
+          const float f = sm.fac[p][hh];
+          t.x = fmaf(y[u].x, f, t.x);
+          t.y = fmaf(y[u].y, f, t.y);
+          t.z = fmaf(y[u].z, f, t.z);
+          t.w = fmaf(y[u].w, f, t.w);
+        }
+      }
+      if (p0 + kBatch * groups < parts) load(p0 + kBatch * groups);
+    }
+  }
+  float4* const scratch = reinterpret_cast<float4*>(&sm.sums[0][0][0]);
+  scratch[tid] = t;
+  __syncthreads();
+  if (gr == 0) {
+    for (int g = 1; g < groups; ++g) {
+      const float4 x = scratch[g * cols + ci];
+      t.x += x.x;
+      t.y += x.y;
+      t.z += x.z;
+      t.w += x.w;
+    }
+    const float f = sm.fin[hh][3];
+    reinterpret_cast<float4*>(a.out + (unit * a.G + hh) * kD)[d4] =
+        make_float4(t.x * f, t.y * f, t.z * f, t.w * f);
+  }
+}
+
+// FMT: byte format; NT: value products per 16 keys (1: G <= 4, 2: G <= 8).
+template <typename T, int FMT, int NT, bool kUni>
+__global__ void __launch_bounds__(kThr, 1) kv8_attention_kernel(const Args a) {
+  constexpr bool kLo = sizeof(T) == 4;   // fp32 queries take two fp16 parts
+  using S = Smem<NT>;
+  __shared__ __align__(16) S sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gid = lane >> 2, q = lane & 3;
-  const int C0 = gridDim.x;
   pdl_wait();
   pdl_trigger();
 
   // ---- this CTA's steps [s0, s1) of the line of all units' steps
-  long long T_all, s0, s1;
-  int C;
+  int s0, s1, C;
+  Cut cut;
   Place pf;
+  const auto cut_line = [&](int steps) {
+    C = min(int(gridDim.x), steps);
+    cut.q = C > 0 ? steps / C : 0;
+    cut.r = steps - cut.q * C;
+    const int cta = min(int(blockIdx.x), C);
+    s0 = cut.start(cta);
+    s1 = cut.start(min(cta + 1, C));
+  };
   if (a.idx != nullptr || a.seq_lens == nullptr) {
     pf.len = unit_len(a, 0, false);
     pf.ns = steps_of(pf.len);
-    T_all = (long long)(a.c.B) * a.U * pf.ns;
-    C = int(min((long long)C0, T_all));
-    const int cta = min(int(blockIdx.x), C);
-    s0 = T_all * cta / C;
-    s1 = T_all * min(cta + 1, C) / C;
-    const long long u = s0 / pf.ns;
-    pf.ls = int(s0 - u * pf.ns);
-    pf.b = int(u / a.U);
-    pf.j = int(u - (long long)(pf.b) * a.U);
+    cut_line(a.c.B * a.U * pf.ns);
+    const int u = s0 / pf.ns;
+    pf.ls = s0 - u * pf.ns;
+    pf.b = u / a.U;
+    pf.j = u - pf.b * a.U;
   } else {
-    long long mine = 0;
-    for (int b = tid; b < a.c.B; b += kAtThreads)
-      mine += steps_of(unit_len(a, b, blockIdx.x == 0));
+    // every warp for itself: lane l sums sequences l, l + 32, ..., then prefix sums over 32
+    // sequences at a time find the one that holds step s0
+    int mine = 0;
+    for (int b = lane; b < a.c.B; b += 32)
+      mine += steps_of(unit_len(a, b, blockIdx.x == 0 && warp == 0));
+    cut_line(__reduce_add_sync(0xffffffffu, mine) * a.U);
+    int before = 0;
+    for (int b0 = 0; s0 < s1; b0 += 32) {
+      const int b = b0 + lane;
+      const int full = b < a.c.B ? unit_len(a, b, false) : 0;
+      const int n = steps_of(full) * a.U;
+      int inc = n;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    long long* const tot = reinterpret_cast<long long*>(&sm.sums[0][0][0]);
-    if (lane == 0) tot[warp] = mine;
-    __syncthreads();
-    T_all = 0;
-#pragma unroll
-    for (int w = 0; w < kAtWarps; ++w) T_all += tot[w];
-    T_all *= a.U;
-    C = int(min((long long)C0, T_all));
-    const int cta = min(int(blockIdx.x), C);
-    s0 = C > 0 ? T_all * cta / C : 0;
-    s1 = C > 0 ? T_all * min(cta + 1, C) / C : 0;
-    if (warp == 0 && s0 < s1) {
-      // the sequence that holds step s0: prefix sums, 32 sequences at a time
-      long long before = 0;
-      for (int b0 = 0;; b0 += 32) {
-        const int b = b0 + lane;
-        const long long n = b < a.c.B ? (long long)(steps_of(unit_len(a, b, false))) * a.U : 0;
-        long long inc = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += y;
-        }
-        const unsigned hit = __ballot_sync(0xffffffffu, before + inc > s0);
-        if (hit) {
-          const int l = __ffs(hit) - 1;
-          if (lane == l) {
-            sm.first_b = b;
-            sm.base = before + inc - n;
-          }
-          break;
-        }
-        before += __shfl_sync(0xffffffffu, inc, 31);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
       }
-    }
-    __syncthreads();
-    if (s0 < s1) {
-      pf.b = sm.first_b;
-      pf.len = unit_len(a, pf.b, false);
-      pf.ns = steps_of(pf.len);
-      const long long r = s0 - sm.base;
-      pf.j = int(r / pf.ns);
-      pf.ls = int(r - (long long)(pf.j) * pf.ns);
+      const unsigned hit = __ballot_sync(0xffffffffu, before + inc > s0);
+      if (hit) {
+        const int at = __ffs(hit) - 1;
+        pf.b = b0 + at;
+        pf.len = __shfl_sync(0xffffffffu, full, at);
+        pf.ns = steps_of(pf.len);
+        const int r = s0 - (before + __shfl_sync(0xffffffffu, inc - n, at));
+        pf.j = r / pf.ns;
+        pf.ls = r - pf.j * pf.ns;
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
     }
     // sequences of length zero: their outputs are zero
-    for (int b = blockIdx.x; b < a.c.B; b += C0) {
+    for (int b = blockIdx.x; b < a.c.B; b += gridDim.x) {
       if (unit_len(a, b, false) != 0) continue;
-      for (int i = tid; i < a.U * a.G * kD; i += kAtThreads)
+      for (int i = tid; i < a.U * a.G * kD; i += kThr)
         a.out[int64_t(b) * a.U * a.G * kD + i] = 0.0f;
       if (a.stats != nullptr)
-        for (int i = tid; i < a.U * a.G * 2; i += kAtThreads)
+        for (int i = tid; i < a.U * a.G * 2; i += kThr)
           a.stats[int64_t(b) * a.U * a.G * 2 + i] = 0.0f;
     }
   }
   if (s0 >= s1) return;
+  const int head = NT == 1 ? (gid & 3) : gid;       // this lane's head row
+  const bool head_ok = head < a.G;
+  // the queries first: they are needed as soon as the first keys are
+  QueryRow<T> qrow;
+  qrow.load(a.q, (int64_t(pf.b) * a.U + pf.j) * a.G + head, head_ok, q);
 
-  // ---- ring: fetch rows one tile ahead of their copies, copies ST - 1 tiles ahead
-  const uint32_t ring0 = smem_addr(&sm.ring[warp][0][0]);
-  const uint32_t scale0 = smem_addr(&sm.scale[warp][0][0]);
-  long long fetched = s0;
-  int64_t row_next = key_row(a, pf, warp, lane & 15);
-  const auto issue = [&](int st) {
-    const int64_t row = row_next;
-    const unsigned there = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
-    if (lane == 0) sm.mask[warp][st] = there;
-    const uint32_t base = ring0 + st * kTileBytes;
+  // ---- loads.  Half u of a tile: kreg[u][2 tau + j] is key 8 tau + gid, bytes 16 (4 j + q);
+  // vreg[u][i] key 8 (i / 2) + 2 q + i % 2, bytes 16 gid; the scales of those keys (kUni: the half's)
+  constexpr int kSc = kUni ? 1 : 4;
+  uint4 kreg[2][4], vreg[2][4];
+  float ksc[2][kSc], vsc[2][kSc];
+  const auto load_k_of = [&](const Rows& r, auto full) {
+    constexpr bool kFull = decltype(full)::value;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 4 * i + (lane >> 3);
-      const int64_t rr = __shfl_sync(0xffffffffu, row, r);
-      const bool ok = rr >= 0;
-      const int64_t off = (ok ? rr : 0) * kD + 16 * (lane & 7);
-      const uint32_t dst = base + r * kD + 16 * ((lane & 7) ^ swz(r));
-      cp_async_16_or_zero(dst, a.c.k + off, ok);
-      cp_async_16_or_zero(dst + kTile * kD, a.c.v + off, ok);
+    for (int u = 0; u < 2; ++u) {
+      [[maybe_unused]] const uint32_t there = r.mask >> (16 * u);
+      if constexpr (kUni) {
+        const uint8_t* const p = a.c.k + int64_t(r.row[u]) * kD + gid * kD + 16 * q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          kreg[u][i] = load_row16(p + (i >> 1) * 8 * kD + (i & 1) * 64,
+                                  kFull || ((there >> (8 * (i >> 1) + gid)) & 1u));
+        ksc[u][0] =
+            kFull || (there & 0xffffu) ? __ldg(a.c.ks + (r.row[u] >> a.c.bshift)) : 0.0f;
+      } else {
+#pragma unroll
+        for (int tau = 0; tau < 2; ++tau) {
+          const int row = __shfl_sync(0xffffffffu, r.row[0], 16 * u + 8 * tau + gid);
+          const uint8_t* const p = a.c.k + int64_t(row) * kD + 16 * q;
+          kreg[u][2 * tau] = load_row16(p, kFull || row >= 0);
+          kreg[u][2 * tau + 1] = load_row16(p + 64, kFull || row >= 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = __shfl_sync(0xffffffffu, r.row[0], 16 * u + 8 * (i >> 1) + 2 * q + (i & 1));
+          ksc[u][kUni ? 0 : i] = kFull || row >= 0 ? __ldg(a.c.ks + (row >> a.c.bshift)) : 0.0f;
+        }
+      }
     }
-    const bool ok = row >= 0;
-    cp_async_4_or_zero(scale0 + (st * 2 * kTile + lane) * 4,
-                       (lane < 16 ? a.c.ks : a.c.vs) + ((ok ? row : 0) >> a.c.bshift), ok);
-    cp_async_commit();
   };
-  const auto fetch = [&]() {
-    ++fetched;
-    if (fetched < s1) {
-      next_place(a, pf);
-      row_next = key_row(a, pf, warp, lane & 15);
+  const auto load_v_of = [&](const Rows& r, auto full) {
+    constexpr bool kFull = decltype(full)::value;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      [[maybe_unused]] const uint32_t there = r.mask >> (16 * u);
+      if constexpr (kUni) {
+        const uint8_t* const p = a.c.v + int64_t(r.row[u]) * kD + 2 * q * kD + 16 * gid;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          vreg[u][i] = load_row16(p + (i >> 1) * 8 * kD + (i & 1) * kD,
+                                  kFull || ((there >> (8 * (i >> 1) + 2 * q + (i & 1))) & 1u));
+        vsc[u][0] =
+            kFull || (there & 0xffffu) ? __ldg(a.c.vs + (r.row[u] >> a.c.bshift)) : 0.0f;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = __shfl_sync(0xffffffffu, r.row[0], 16 * u + 8 * (i >> 1) + 2 * q + (i & 1));
+          vreg[u][i] = load_row16(a.c.v + int64_t(row) * kD + 16 * gid, kFull || row >= 0);
+          vsc[u][kUni ? 0 : i] = kFull || row >= 0 ? __ldg(a.c.vs + (row >> a.c.bshift)) : 0.0f;
+        }
+      }
     }
   };
+  const auto load_k = [&](const Rows& r) {
+    if (r.mask == 0xffffffffu) load_k_of(r, std::true_type{});
+    else load_k_of(r, std::false_type{});
+  };
+  const auto load_v = [&](const Rows& r) {
+    if (r.mask == 0xffffffffu) load_v_of(r, std::true_type{});
+    else load_v_of(r, std::false_type{});
+  };
+  // lane i pulls key i's K and V rows (one 128-byte line each) into L2
+  const auto pull = [&](const Rows& r) {
+    const int row = kUni ? (lane < 16 ? r.row[0] : r.row[1] - 16) + lane : r.row[0];
+    if ((r.mask >> lane) & 1u) {
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.k + int64_t(row) * kD));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.v + int64_t(row) * kD));
+    }
+  };
+
+  // Tiles under way: r0 in registers (or coming), r1 the next one, tb with its pages and ta with
+  // its positions coming.
   Place cur = pf;
-#pragma unroll
-  for (int st = 0; st < ST - 1; ++st) {
-    if (fetched < s1) {
-      issue(st);
-      fetch();
-    } else {
-      cp_async_commit();
-    }
+  int placed = s0;
+  const auto next_tile = [&]() {
+    if (++placed >= s1) return no_tile();
+    next_place(a, pf);
+    return tile_positions<kUni>(a, pf, warp, lane);
+  };
+  Rows r0, r1;
+  Tile ta, tb;
+  {
+    Tile t0 = tile_positions<kUni>(a, pf, warp, lane), t1 = next_tile();
+    tb = next_tile();
+    ta = next_tile();
+    tile_pages<kUni>(a, t0);
+    tile_pages<kUni>(a, t1);
+    tile_pages<kUni>(a, tb);
+    r0 = tile_rows<kUni>(a, t0);
+    load_k(r0);
+    load_v(r0);
+    r1 = tile_rows<kUni>(a, t1);
+    pull(r1);
   }
+  const auto fetch = [&]() {
+    const Rows r = tile_rows<kUni>(a, tb);
+    pull(r);
+    tb = ta;
+    tile_pages<kUni>(a, tb);
+    ta = next_tile();
+    return r;
+  };
 
   uint32_t qh[8][2], ql[kLo ? 8 : 1][2];
   float factor = 0.0f;
   float m = -INFINITY, m2 = -INFINITY, l = 0.0f;
-  float acc[NT][8][4];
-  const int head = NT == 1 ? (gid & 3) : gid;       // this lane's head row
-  const bool head_ok = head < a.G;
+  float acc[8][4];
   bool fresh = true;
-  int st = 0;
-  for (long long s = s0; s < s1; ++s) {
-    {
-      int sn = st + ST - 1;
-      if (sn >= ST) sn -= ST;
-      if (fetched < s1) {
-        issue(sn);
-        fetch();
-      } else {
-        cp_async_commit();
-      }
-    }
+  int64_t open_unit[2] = {0, 0};   // units this CTA holds a part of
+  int open_u0[2] = {0, 0}, open_parts[2] = {0, 0};
+  uint32_t before[2] = {0u, 0u};
+  for (int s = s0; s < s1; ++s) {
     const int64_t unit = int64_t(cur.b) * a.U + cur.j;
     if (fresh) {
-      factor = load_q<T, kLo>(a, unit * a.G + head, head_ok, q, qh, ql);
+      factor = query_fragments<T, kLo>(qrow, a.scale_log2, qh, ql);
       m = m2 = -INFINITY;
       l = 0.0f;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[n][t][i] = 0.0f;
+        for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
       fresh = false;
     }
-    cp_async_wait_pending(ST - 1);
-    __syncwarp();
-    const uint32_t mask = sm.mask[warp][st];
-    if (mask != 0) {
-      const uint8_t* const tile = sm.ring[warp][st];
-      const float* const sc = sm.scale[warp][st];
-      // ---- scores of keys 8 tau + 2 q + {0, 1}, tau = 0, 1
-      float x[4], sf[4];
+    Rows r2;
+    // kFull: all 32 keys are there
+    const auto attend = [&](auto full) {
+      constexpr bool kFull = decltype(full)::value;
+      const uint32_t mask = r0.mask >> (2 * q);
+      const auto there = [&](int u, int i) {   // key 16 u + 8 (i / 2) + 2 q + i % 2
+        return kFull || ((mask >> (16 * u + 8 * (i >> 1) + (i & 1))) & 1u);
+      };
+      // ---- scores x (before scaling) of keys 16 u + 8 tau + 2 q + {0, 1}
+      float x[2][4], sf[2][kSc];
 #pragma unroll
-      for (int tau = 0; tau < 2; ++tau) {
-        const int r = 8 * tau + gid;
-        float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int u = 0; u < 2; ++u) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint4 w =
-              *reinterpret_cast<const uint4*>(tile + r * kD + 16 * ((4 * j + q) ^ swz(r)));
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        for (int tau = 0; tau < 2; ++tau) {
+          float cc[2][4];   // two chains: dimensions 0..63 and 64..127
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = 4 * j + i;
-            const uint32_t b0 = half2_of<FMT>(ww[i], 0), b1 = half2_of<FMT>(ww[i], 1);
-            const uint32_t l0 = kLo ? ql[kLo ? c : 0][0] : 0u, l1 = kLo ? ql[kLo ? c : 0][1] : 0u;
-            if (j == 0) mma_f16(c0, qh[c][0], l0, qh[c][1], l1, b0, b1);
-            else mma_f16(c1, qh[c][0], l0, qh[c][1], l1, b0, b1);
+          for (int j = 0; j < 2; ++j) {
+            const uint4 w = kreg[u][2 * tau + j];
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int c = 4 * j + i;
+              const uint32_t b0 = half2_of<FMT>(ww[i], 0), b1 = half2_of<FMT>(ww[i], 1);
+              const uint32_t l0 = kLo ? ql[kLo ? c : 0][0] : 0u;
+              const uint32_t l1 = kLo ? ql[kLo ? c : 0][1] : 0u;
+              if (i == 0) mma_f16_first(cc[j], qh[c][0], l0, qh[c][1], l1, b0, b1);
+              else mma_f16(cc[j], qh[c][0], l0, qh[c][1], l1, b0, b1);
+            }
           }
-        }
-        const float2 ks = *reinterpret_cast<const float2*>(sc + 8 * tau + 2 * q);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float dot = kLo ? (c0[e] + c1[e]) + (c0[2 + e] + c1[2 + e]) : c0[e] + c1[e];
-          sf[2 * tau + e] = (e ? ks.y : ks.x) * factor;
-          x[2 * tau + e] = dot;
+          for (int e = 0; e < 2; ++e)
+            x[u][2 * tau + e] =
+                kLo ? (cc[0][e] + cc[1][e]) + (cc[0][2 + e] + cc[1][2 + e]) : cc[0][e] + cc[1][e];
         }
+#pragma unroll
+        for (int i = 0; i < kSc; ++i) sf[u][i] = ksc[u][i] * factor;
       }
-      // ---- references
-      float vs[4];
-      *reinterpret_cast<float2*>(vs) = *reinterpret_cast<const float2*>(sc + kTile + 2 * q);
-      *reinterpret_cast<float2*>(vs + 2) = *reinterpret_cast<const float2*>(sc + kTile + 8 + 2 * q);
-      bool there[4];
-      float mn = m, m2n = m2;
+      load_k(r1);
+      // ---- references.  The value scale's exponent is rounded up, and taken as at least -112
+      // so that 2^14 times its reciprocal is finite.
+      float up = -INFINITY, up2 = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        there[i] = (mask >> (8 * (i >> 1) + 2 * q + (i & 1))) & 1u;
-        const float up = there[i] ? ceilf(x[i] * sf[i]) : -INFINITY;
-        mn = fmaxf(mn, up);
-        // exponent of the value scale, rounded up, at least -112 so that 2^14 times its
-        // reciprocal is finite
-        m2n = fmaxf(m2n, up + float(max(int(__float_as_uint(vs[i]) >> 23) - 126, -112)));
+      for (int u = 0; u < 2; ++u) {
+        float half = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float y = there(u, i) ? x[u][i] * sf[u][kUni ? 0 : i] : -INFINITY;
+          half = fmaxf(half, y);
+          if (!kUni)
+            up2 = fmaxf(up2, y + float(max(int(__float_as_uint(vsc[u][kUni ? 0 : i]) >> 23) - 126,
+                                           -112)));
+        }
+        up = fmaxf(up, half);
+        if (kUni)
+          up2 = fmaxf(up2, half + float(max(int(__float_as_uint(vsc[u][0]) >> 23) - 126, -112)));
       }
       if (a.scores != nullptr && (NT == 2 || gid < 4) && head_ok) {
         float* const o = a.scores + (unit * a.G + head) * a.score_stride + cur.ls * kStep +
                          warp * kTile + 2 * q;
-        float y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = there[i] ? x[i] * sf[i] : -INFINITY;
-        *reinterpret_cast<float2*>(o) = make_float2(y[0], y[1]);
-        *reinterpret_cast<float2*>(o + 8) = make_float2(y[2], y[3]);
+        for (int u = 0; u < 2; ++u) {
+          float y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = there(u, i) ? x[u][i] * sf[u][kUni ? 0 : i] : -INFINITY;
+          *reinterpret_cast<float2*>(o + 16 * u) = make_float2(y[0], y[1]);
+          *reinterpret_cast<float2*>(o + 16 * u + 8) = make_float2(y[2], y[3]);
+        }
       }
-      mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 1));
-      m2n = fmaxf(m2n, __shfl_xor_sync(0xffffffffu, m2n, 1));
-      mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 2));
-      m2n = fmaxf(m2n, __shfl_xor_sync(0xffffffffu, m2n, 2));
-      if (__any_sync(0xffffffffu, mn > m || m2n > m2)) {
+      up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 1));
+      up2 = fmaxf(up2, __shfl_xor_sync(0xffffffffu, up2, 1));
+      up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 2));
+      up2 = fmaxf(up2, __shfl_xor_sync(0xffffffffu, up2, 2));
+      if (__any_sync(0xffffffffu, up > m || up2 > m2)) {
+        const float mn = fmaxf(m, ceilf(up)), m2n = fmaxf(m2, ceilf(up2));
         l *= ref_change(m, mn);
         const float r = ref_change(m2, m2n);
-        const float r0 = __shfl_sync(0xffffffffu, r, 8 * q);       // column 2 q
-        const float r1 = __shfl_sync(0xffffffffu, r, 8 * q + 4);   // column 2 q + 1
+        const float f0 = __shfl_sync(0xffffffffu, r, 8 * q);       // column 2 q
+        const float f1 = __shfl_sync(0xffffffffu, r, 8 * q + 4);   // column 2 q + 1
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            acc[n][t][0] *= r0;
-            acc[n][t][1] *= r1;
-            acc[n][t][2] *= r0;
-            acc[n][t][3] *= r1;
-          }
+        for (int t = 0; t < 8; ++t) {
+          acc[t][0] *= f0;
+          acc[t][1] *= f1;
+          acc[t][2] *= f0;
+          acc[t][3] *= f1;
+        }
         m = mn;
         m2 = m2n;
       }
       // w = 2^(x - m) c 2^(m - m2 + 14)
       const float lift = m2 == -INFINITY ? 1.0f : ex2(m - m2 + kWBias);
-      float w[4];
+      uint32_t b[2][NT][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p = there[i] ? ex2(fmaf(x[i], sf[i], -m)) : 0.0f;
-        l += p;
-        w[i] = p * (vs[i] * lift);
-      }
-      uint32_t b0[NT], b1[NT];
-      b0[0] = pack_f16(w[0], w[1]);
-      b1[0] = pack_f16(w[2], w[3]);
-      if constexpr (NT == 1) {
-        if (gid >= 4) {   // columns 4..7: the low parts of heads 0..3
-          b0[0] = pack_f16_rest(w[0], w[1], b0[0]);
-          b1[0] = pack_f16_rest(w[2], w[3], b1[0]);
+      for (int u = 0; u < 2; ++u) {
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = there(u, i) ? ex2(fmaf(x[u][i], sf[u][kUni ? 0 : i], -m)) : 0.0f;
+          l += p;
+          w[i] = p * (vsc[u][kUni ? 0 : i] * lift);
         }
-      } else {
-        b0[NT - 1] = pack_f16_rest(w[0], w[1], b0[0]);
-        b1[NT - 1] = pack_f16_rest(w[2], w[3], b1[0]);
+        b[u][0][0] = pack_f16(w[0], w[1]);
+        b[u][0][1] = pack_f16(w[2], w[3]);
+        if constexpr (NT == 1) {
+          // columns 4..7: the low parts of heads 0..3
+          const uint32_t e0 = pack_f16_rest(w[0], w[1], b[u][0][0]);
+          const uint32_t e1 = pack_f16_rest(w[2], w[3], b[u][0][1]);
+          b[u][0][0] = gid >= 4 ? e0 : b[u][0][0];
+          b[u][0][1] = gid >= 4 ? e1 : b[u][0][1];
+        } else {
+          b[u][NT - 1][0] = pack_f16_rest(w[0], w[1], b[u][0][0]);
+          b[u][NT - 1][1] = pack_f16_rest(w[2], w[3], b[u][0][1]);
+        }
       }
+      r2 = fetch();
       // ---- values: lane (gid, q): dimensions 16 gid .. + 15 of keys 2q, 2q+1, 8+2q, 9+2q
-      uint4 v[4];
+      // A tile's product is formed by itself and added in fp32: the tensor cores' own sums drop
+      // bits below the sum's last, always towards zero, which over thousands of keys shows (2.1e-6
+      // of the result at 128K keys per head against 1.0e-6 of fp32 sums).
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = 8 * (i >> 1) + 2 * q + (i & 1);
-        v[i] = *reinterpret_cast<const uint4*>(tile + (kTile + r) * kD + 16 * (gid ^ swz(r)));
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t ka = i == 0 ? v[0].x : i == 1 ? v[0].y : i == 2 ? v[0].z : v[0].w;
-        const uint32_t kb = i == 0 ? v[1].x : i == 1 ? v[1].y : i == 2 ? v[1].z : v[1].w;
-        const uint32_t kc = i == 0 ? v[2].x : i == 1 ? v[2].y : i == 2 ? v[2].z : v[2].w;
-        const uint32_t kd = i == 0 ? v[3].x : i == 1 ? v[3].y : i == 2 ? v[3].z : v[3].w;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const uint32_t ab = __byte_perm(ka, kb, hf ? 0x7362 : 0x5140);
-          const uint32_t cd = __byte_perm(kc, kd, hf ? 0x7362 : 0x5140);
-          const uint32_t a0 = half2_of<FMT>(ab, 0), a1 = half2_of<FMT>(ab, 1);
-          const uint32_t a2 = half2_of<FMT>(cd, 0), a3 = half2_of<FMT>(cd, 1);
+          float part[4];
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(acc[n][2 * i + hf], a0, a1, a2, a3, b0[n], b1[n]);
+          for (int u = 0; u < 2; ++u) {
+            const auto word = [&](int v) {
+              return i == 0 ? vreg[u][v].x : i == 1 ? vreg[u][v].y : i == 2 ? vreg[u][v].z
+                                                                            : vreg[u][v].w;
+            };
+            const uint32_t ab = __byte_perm(word(0), word(1), hf ? 0x7362 : 0x5140);
+            const uint32_t cd = __byte_perm(word(2), word(3), hf ? 0x7362 : 0x5140);
+            const uint32_t a0 = half2_of<FMT>(ab, 0), a1 = half2_of<FMT>(ab, 1);
+            const uint32_t a2 = half2_of<FMT>(cd, 0), a3 = half2_of<FMT>(cd, 1);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              if (u == 0 && n == 0) mma_f16_first(part, a0, a1, a2, a3, b[u][n][0], b[u][n][1]);
+              else mma_f16(part, a0, a1, a2, a3, b[u][n][0], b[u][n][1]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[2 * i + hf][e] += part[e];
         }
       }
+      load_v(r1);
+    };
+    if (r0.mask == 0xffffffffu) {
+      attend(std::true_type{});
+    } else if (r0.mask != 0u) {
+      attend(std::false_type{});
+    } else {
+      if (a.scores != nullptr) {
+        // entries without a key (skipped, or a bad page) have no weight
+        for (int i = lane; i < a.G * kTile; i += 32) {
+          const int at = cur.ls * kStep + warp * kTile + i % kTile;
+          if (at < cur.len)
+            a.scores[(unit * a.G + i / kTile) * a.score_stride + at] = -INFINITY;
+        }
+      }
+      load_k(r1);
+      r2 = fetch();
+      load_v(r1);
     }
-    if (mask == 0 && a.scores != nullptr && cur.ls * kStep + warp * kTile < cur.len) {
-      // entries without a key (skipped, or a bad page) have no weight
-      for (int i = lane; i < a.G * kTile; i += 32)
-        a.scores[(unit * a.G + i / kTile) * a.score_stride + cur.ls * kStep + warp * kTile +
-                 i % kTile] = -INFINITY;
-    }
-    __syncwarp();   // the tile's buffer is refilled by the next iteration
-    if (++st == ST) st = 0;
+    r0 = r1;
+    r1 = r2;
 
-    const bool unit_ends = cur.ls + 1 == cur.ns;
-    if (unit_ends || s + 1 == s1) {
+    const int u0 = s - cur.ls;                  // the unit's first step
+    const int unit_end = u0 + cur.ns;
+    if (s + 1 < s1 && s + 1 < unit_end) {
+      ++cur.ls;
+    } else {
+      if (s + 1 < s1) {
+        // the next unit's queries come while this one's states are merged
+        next_place(a, cur);
+        qrow.load(a.q, (int64_t(cur.b) * a.U + cur.j) * a.G + head, head_ok, q);
+      }
       // ---- merge the warps' states
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
@@ -524,199 +794,126 @@ __global__ void __launch_bounds__(kAtThreads, kMinBlocks) kv8_attention_kernel(c
         sm.stat[warp][head][2] = m2;
       }
       __syncthreads();
-      float M = -INFINITY, M2 = -INFINITY, Ls = 0.0f;
+      float M2 = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kAtWarps; ++w) {
-        M = fmaxf(M, sm.stat[w][head][0]);
-        M2 = fmaxf(M2, sm.stat[w][head][2]);
-      }
-#pragma unroll
-      for (int w = 0; w < kAtWarps; ++w) Ls += sm.stat[w][head][1] * ref_change(sm.stat[w][head][0], M);
+      for (int w = 0; w < kWarps; ++w) M2 = fmaxf(M2, sm.stat[w][head][2]);
       {
         const float r = ref_change(m2, M2);
-        const float r0 = __shfl_sync(0xffffffffu, r, 8 * q);
-        const float r1 = __shfl_sync(0xffffffffu, r, 8 * q + 4);
+        const float f0 = __shfl_sync(0xffffffffu, r, 8 * q);
+        const float f1 = __shfl_sync(0xffffffffu, r, 8 * q + 4);
+        // High and low parts together, at the merged reference.  NT = 1: lanes q and q ^ 2
+        // hold the two parts of two heads; each keeps half of the dimensions (value 4 t + i:
+        // tile t + 4 (q / 2)).  NT = 2: value 4 t + i: tile t.
+        if constexpr (NT == 1) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            acc[n][t][0] *= r0;
-            acc[n][t][1] *= r1;
-            acc[n][t][2] *= r0;
-            acc[n][t][3] *= r1;
-          }
-      }
-      // high and low parts together: NT = 1, lanes q and q ^ 2 hold the two parts of two
-      // heads; each keeps half of the dimensions (value 4 t + i: tile t + 4 (q >> 1)).
-      // NT = 2: both parts are in the lane (value 4 t + i: tile t).
-      float val[S::kSums];
-      if constexpr (NT == 1) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float keep = (q & 2) ? acc[0][t + 4][i] : acc[0][t][i];
-            const float give = (q & 2) ? acc[0][t][i] : acc[0][t + 4][i];
-            val[4 * t + i] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
-          }
-      } else {
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) val[4 * t + i] = acc[0][t][i] + acc[NT - 1][t][i];
-      }
-#pragma unroll
-      for (int h = kAtWarps / 2; h > 0; h >>= 1) {
-        if (warp >= h && warp < 2 * h) {
-#pragma unroll
-          for (int i = 0; i < S::kSums; ++i) sm.sums[warp - h][i][lane] = val[i];
-        }
-        __syncthreads();
-        if (warp < h) {
-#pragma unroll
-          for (int i = 0; i < S::kSums; ++i) val[i] += sm.sums[warp][i][lane];
-        }
-        __syncthreads();
-      }
-      // ---- the unit's parts: CTAs c0 .. c1 hold steps of it
-      const long long u0 = s - cur.ls;                          // the unit's first step
-      const int c0 = int(((u0 + 1) * C + T_all - 1) / T_all) - 1;
-      const int c1 = int(((u0 + cur.ns) * C + T_all - 1) / T_all) - 1;
-      const int parts = c1 - c0 + 1;
-      const int cta = blockIdx.x;
-      if (warp == 0) {
-        // dimensions of this lane's values: 16 gid + d0 + 0..7 for NT = 1, + 0..15 for NT = 2;
-        // head of column 2 (q or q & 1) + (i & 1)
-        constexpr int kRun = S::kSums / 2;
-        const int col = NT == 1 ? 2 * (q & 1) : 2 * q;
-        const int dim = 16 * gid + (NT == 1 ? 8 * (q >> 1) : 0);
-        if (parts == 1) {
-          // factor of head `head`, held by the lanes of row gid = head
-          const float f = Ls > 0.0f || !(Ls == Ls) ? ex2(M2 - M - kWBias) / Ls : 0.0f;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float fe = __shfl_sync(0xffffffffu, f, 4 * (col + e));
-            if (col + e < a.G) {
-              float* const o = a.out + (unit * a.G + col + e) * kD + dim;
-#pragma unroll
-              for (int d = 0; d < kRun; d += 4)
-                *reinterpret_cast<float4*>(o + d) =
-                    make_float4(val[2 * d + e] * fe, val[2 * d + 2 + e] * fe,
-                                val[2 * d + 4 + e] * fe, val[2 * d + 6 + e] * fe);
+            for (int i = 0; i < 4; ++i) {
+              const float keep = (q & 2) ? acc[t + 4][i] : acc[t][i];
+              const float give = (q & 2) ? acc[t][i] : acc[t + 4][i];
+              sm.sums[warp][4 * t + i][lane] =
+                  (keep + __shfl_xor_sync(0xffffffffu, give, 2)) * ((i & 1) ? f1 : f0);
             }
-          }
-          if (a.stats != nullptr && q == 0 && gid < a.G && (NT == 2 || gid < 4)) {
-            float* const o = a.stats + (unit * a.G + gid) * 2;
-            const bool some = Ls > 0.0f || !(Ls == Ls);
-            o[0] = some ? M : 0.0f;
-            o[1] = some ? 1.0f / Ls : 0.0f;
+        } else {
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              sm.sums[warp][4 * t + i][lane] =
+                  acc[t][i] * ((i & 1) ? f1 : f0);
+        }
+      }
+      if (warp < a.G) {   // head `warp`: lane w takes warp w's state
+        const float wm = lane < kWarps ? sm.stat[lane % kWarps][warp][0] : -INFINITY;
+        const float wl = lane < kWarps ? sm.stat[lane % kWarps][warp][1] : 0.0f;
+        const float wm2 = lane < kWarps ? sm.stat[lane % kWarps][warp][2] : -INFINITY;
+        float hM = wm, hM2 = wm2;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          hM = fmaxf(hM, __shfl_xor_sync(0xffffffffu, hM, o));
+          hM2 = fmaxf(hM2, __shfl_xor_sync(0xffffffffu, hM2, o));
+        }
+        const float hl = warp_sum(wl * ref_change(wm, hM));
+        if (lane == 0) {
+          const bool some = hl > 0.0f || !(hl == hl);   // an empty list: zeros
+          sm.fin[warp][0] = hM;
+          sm.fin[warp][1] = hM2;
+          sm.fin[warp][2] = hl;
+          sm.fin[warp][3] = some ? ex2(hM2 - hM - kWBias) / hl : 0.0f;
+        }
+      }
+      __syncthreads();
+      // ---- the unit's parts: CTAs c0 .. c0 + parts - 1 hold steps of it
+      const int c0 = cut.owner(u0);
+      const int parts = cut.owner(unit_end - 1) - c0 + 1;
+      // slot 0: the CTA's first unit, slot 1: its last when that is another one
+      float* const slot = a.part + int64_t(2 * blockIdx.x + (u0 > s0 ? 1 : 0)) * a.G * kPart;
+      // value v of lane (gid, q) of the fragments: head 2 q (NT = 1: 2 (q % 2)) + v % 2,
+      // dimension 16 gid (+ 8 (q / 2)) + v / 2; thread (head, 4 dimensions) sums the warps
+      for (int i = tid; i < a.G * (kD / 4); i += kThr) {
+        const int hh = i / (kD / 4), d = 4 * (i % (kD / 4));
+        const int ln = 4 * (d >> 4) + (NT == 1 ? (hh >> 1) + 2 * ((d >> 3) & 1) : hh >> 1);
+        const int v0 = 2 * (NT == 1 ? d & 7 : d & 15) + (hh & 1);
+        float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) t[e] += sm.sums[w][v0 + 2 * e][ln];
+        if (parts == 1) {
+          const float f = sm.fin[hh][3];
+          *reinterpret_cast<float4*>(a.out + (unit * a.G + hh) * kD + d) =
+              make_float4(t[0] * f, t[1] * f, t[2] * f, t[3] * f);
+        } else {
+          *reinterpret_cast<float4*>(slot + hh * kPart + 4 + d) =
+              make_float4(t[0], t[1], t[2], t[3]);
+        }
+      }
+      if (tid < a.G) {
+        if (parts == 1) {
+          if (a.stats != nullptr) {
+            float* const o = a.stats + (unit * a.G + tid) * 2;
+            const float hl = sm.fin[tid][2];
+            const bool some = hl > 0.0f || !(hl == hl);
+            o[0] = some ? sm.fin[tid][0] : 0.0f;
+            o[1] = some ? 1.0f / hl : 0.0f;
           }
         } else {
-          // slot 0: the CTA's first unit, slot 1: its last when that is another one
-          const int slot = 2 * cta + (u0 > s0 ? 1 : 0);
-          float* const base = a.part + int64_t(slot) * a.G * kPart;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (col + e < a.G) {
-              float* const o = base + (col + e) * kPart + 4 + dim;
-#pragma unroll
-              for (int d = 0; d < kRun; d += 4)
-                *reinterpret_cast<float4*>(o + d) =
-                    make_float4(val[2 * d + e], val[2 * d + 2 + e], val[2 * d + 4 + e],
-                                val[2 * d + 6 + e]);
-            }
-          }
-          if (q == 0 && gid < a.G && (NT == 2 || gid < 4)) {
-            float* const o = base + gid * kPart;
-            o[0] = M;
-            o[1] = Ls;
-            o[2] = M2;
-          }
-          __threadfence();
-          __syncwarp();
-          if (lane == 0)
-            sm.last = atomicAdd(a.count + unit, 1u) + 1u == uint32_t(parts) ? 1 : 0;
+          float* const o = slot + tid * kPart;
+          o[0] = sm.fin[tid][0];
+          o[1] = sm.fin[tid][2];
+          o[2] = sm.fin[tid][1];
         }
       }
+      __syncthreads();   // the parts are written; sums, stat and fin are free again
       if (parts > 1) {
-        __syncthreads();
-        if (sm.last) {
+        // a CTA has at most two parts: its first unit's and its last unit's.  Whether a unit is
+        // complete is looked at when the CTA is done, so nothing waits for the count here.
+        const int which = u0 > s0 ? 1 : 0;
+        open_unit[which] = unit;
+        open_u0[which] = u0;
+        open_parts[which] = parts;
+        if (tid == 0) {
           __threadfence();
-          const auto slot_of = [&](int p) {
-            const int c = c0 + p;
-            return 2 * c + (p == 0 && T_all * c / C < u0 ? 1 : 0);
-          };
-          if (warp < a.G) {   // head `warp`: references and the sum of weights
-            float hM = -INFINITY, hM2 = -INFINITY;
-            for (int p = lane; p < parts; p += 32) {
-              const float* const o = a.part + (int64_t(slot_of(p)) * a.G + warp) * kPart;
-              hM = fmaxf(hM, __ldcg(o));
-              hM2 = fmaxf(hM2, __ldcg(o + 2));
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-              hM = fmaxf(hM, __shfl_xor_sync(0xffffffffu, hM, o));
-              hM2 = fmaxf(hM2, __shfl_xor_sync(0xffffffffu, hM2, o));
-            }
-            float hl = 0.0f;
-            for (int p = lane; p < parts; p += 32) {
-              const float* const o = a.part + (int64_t(slot_of(p)) * a.G + warp) * kPart;
-              hl += __ldcg(o + 1) * ref_change(__ldcg(o), hM);
-            }
-            hl = warp_sum(hl);
-            if (lane == 0) {
-              const bool some = hl > 0.0f || !(hl == hl);
-              sm.fin[warp][0] = hM2;
-              sm.fin[warp][1] = some ? ex2(hM2 - hM - kWBias) / hl : 0.0f;
-              if (a.stats != nullptr) {
-                float* const o = a.stats + (unit * a.G + warp) * 2;
-                o[0] = some ? hM : 0.0f;
-                o[1] = some ? 1.0f / hl : 0.0f;
-              }
-            }
-          }
-          __syncthreads();
-          // sums: thread = (part group, head, 4 dimensions)
-          const int cols = a.G * (kD / 4);
-          const int groups = kAtThreads / cols;
-          const int gr = tid / cols, ci = tid % cols;
-          const int hh = ci / (kD / 4), d4 = ci % (kD / 4);
-          float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (gr < groups) {
-            const float hM2 = sm.fin[hh][0];
-#pragma unroll 4
-            for (int p = gr; p < parts; p += groups) {
-              const float* const o = a.part + (int64_t(slot_of(p)) * a.G + hh) * kPart;
-              const float f = ref_change(__ldcg(o + 2), hM2);
-              const float4 y = __ldcg(reinterpret_cast<const float4*>(o + 4) + d4);
-              t.x = fmaf(y.x, f, t.x);
-              t.y = fmaf(y.y, f, t.y);
-              t.z = fmaf(y.z, f, t.z);
-              t.w = fmaf(y.w, f, t.w);
-            }
-          }
-          float4* const scratch = reinterpret_cast<float4*>(&sm.sums[0][0][0]);
-          if (gr < groups) scratch[tid] = t;
-          __syncthreads();
-          if (gr == 0) {
-            for (int g = 1; g < groups; ++g) {
-              const float4 y = scratch[g * cols + ci];
-              t.x += y.x;
-              t.y += y.y;
-              t.z += y.z;
-              t.w += y.w;
-            }
-            const float f = sm.fin[hh][1];
-            reinterpret_cast<float4*>(a.out + (unit * a.G + hh) * kD)[d4] =
-                make_float4(t.x * f, t.y * f, t.z * f, t.w * f);
-          }
-          if (tid == 0) a.count[unit] = 0u;
+          before[which] = atomicAdd(a.count + unit, 1u);
         }
-        __syncthreads();   // sm.last and the scratch are free again
       }
       fresh = true;
     }
-    if (s + 1 < s1) next_place(a, cur);
+  }
+  if (open_parts[0] + open_parts[1] == 0) return;
+  if (tid == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      sm.last[i] = open_parts[i] > 0 && before[i] + 1u == uint32_t(open_parts[i]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (!sm.last[i]) continue;
+    __threadfence();
+    combine_parts<NT>(a, sm, cut, open_unit[i], open_u0[i], cut.owner(open_u0[i]), open_parts[i]);
+    if (tid == 0) a.count[open_unit[i]] = 0u;
+    __syncthreads();
   }
 }
 
@@ -804,13 +1001,10 @@ __global__ void __launch_bounds__(512) kv8_sparse_weights_kernel(
   }
 }
 
-constexpr int kStages1 = 3;   // G <= 4: two CTAs of 8 warps per SM
-constexpr int kStages2 = 3;
-
 // CTAs of the attention kernel: the co-resident ones, no more than there can be steps.
-int attention_ctas(int G, int64_t units, int64_t len, int sms) {
+int attention_ctas(int64_t units, int64_t len, int sms) {
   const int64_t steps = units * ((len + kStep - 1) / kStep);
-  const int64_t room = int64_t(sms) * (G <= 4 ? 2 : 1);
+  const int64_t room = sms < kMaxParts ? sms : kMaxParts;
   return int(steps < room ? steps : room);
 }
 
@@ -825,7 +1019,7 @@ Room workspace_room(int B, int Hq, int Hkv, int64_t Lmax, int k, bool shared, bo
   Room r;
   r.count = 256;
   r.part = r.count + align_up(size_t(B) * U * 4, 256);
-  const int ctas = attention_ctas(G, B * U, sparse ? k : Lmax, device_sms());
+  const int ctas = attention_ctas(B * U, sparse ? k : Lmax, device_sms());
   r.stats = r.part + align_up(size_t(ctas) * 2 * G * kPart * 4, 256);
   r.scores = r.stats + (weights ? align_up(size_t(B) * Hq * 8, 256) : 0);
   // rows padded to whole warp tiles: the kernel stores scores tile by tile
@@ -834,30 +1028,25 @@ Room workspace_room(int B, int Hq, int Hkv, int64_t Lmax, int k, bool shared, bo
   return r;
 }
 
-template <typename T, int FMT, int NT, int ST, int MB>
-cudaError_t run_attention(const Args& a, int ctas, cudaStream_t stream) {
-  static std::atomic<uint64_t> done{0};
-  const auto kernel = kv8_attention_kernel<T, FMT, NT, ST, MB>;
-  const int bytes = int(sizeof(Smem<NT, ST>));
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), bytes, done, false);
-  if (e != cudaSuccess) return e;
+template <typename T, int FMT, int NT>
+cudaError_t run_attention(const Args& a, int ctas, bool uni, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas));
-  cfg.blockDim = dim3(kAtThreads);
-  cfg.dynamicSmemBytes = size_t(bytes);
+  cfg.blockDim = dim3(kThr);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return uni ? cudaLaunchKernelEx(&cfg, kv8_attention_kernel<T, FMT, NT, true>, a)
+             : cudaLaunchKernelEx(&cfg, kv8_attention_kernel<T, FMT, NT, false>, a);
 }
 
 template <typename T, int FMT>
-cudaError_t run_attention_g(const Args& a, int ctas, cudaStream_t stream) {
-  if (a.G <= 4) return run_attention<T, FMT, 1, kStages1, 2>(a, ctas, stream);
-  return run_attention<T, FMT, 2, kStages2, 1>(a, ctas, stream);
+cudaError_t run_attention_g(const Args& a, int ctas, bool uni, cudaStream_t stream) {
+  return a.G <= 4 ? run_attention<T, FMT, 1>(a, ctas, uni, stream)
+                  : run_attention<T, FMT, 2>(a, ctas, uni, stream);
 }
 
 }  // namespace
@@ -891,14 +1080,15 @@ cudaError_t launch_kv8_attention(const Kv8& c, int fmt, const void* q, adamas_dt
   a.G = Hq / a.U;
   a.heads_per_kv = a.U / c.Hkv;
   a.k = k;
-  const int ctas = attention_ctas(a.G, int64_t(c.B) * a.U, idx ? k : c.Lmax, device_sms());
+  const int ctas = attention_ctas(int64_t(c.B) * a.U, idx ? k : c.Lmax, device_sms());
+  const bool uni = idx == nullptr && c.bshift >= 4;   // pages are no smaller than blocks
   cudaError_t e;
   if (dt == ADAMAS_BF16)
-    e = fmt == kFmtE4m3 ? run_attention_g<__nv_bfloat16, kFmtE4m3>(a, ctas, stream)
-                        : run_attention_g<__nv_bfloat16, kFmtInt8>(a, ctas, stream);
+    e = fmt == kFmtE4m3 ? run_attention_g<__nv_bfloat16, kFmtE4m3>(a, ctas, uni, stream)
+                        : run_attention_g<__nv_bfloat16, kFmtInt8>(a, ctas, uni, stream);
   else
-    e = fmt == kFmtE4m3 ? run_attention_g<float, kFmtE4m3>(a, ctas, stream)
-                        : run_attention_g<float, kFmtInt8>(a, ctas, stream);
+    e = fmt == kFmtE4m3 ? run_attention_g<float, kFmtE4m3>(a, ctas, uni, stream)
+                        : run_attention_g<float, kFmtInt8>(a, ctas, uni, stream);
   if (e != cudaSuccess || !weights) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;

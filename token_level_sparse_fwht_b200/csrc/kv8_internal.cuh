@@ -92,10 +92,16 @@ template <int FMT>
 __device__ __forceinline__ uint32_t half2_of(uint32_t w, int h) {
   uint32_t r;
   if constexpr (FMT == kFmtE4m3) {
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-        : "=r"(r)
-        : "r"(h ? w >> 16 : w));
+    if (h)
+      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\t"
+          "cvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
+          : "=r"(r)
+          : "r"(w));
+    else
+      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\t"
+          "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+          : "=r"(r)
+          : "r"(w));
   } else {
     const uint32_t f = __byte_perm(w ^ 0x80808080u, 0x64646464u, h ? 0x4342u : 0x4140u);
     asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(f), "r"(0x64806480u));
