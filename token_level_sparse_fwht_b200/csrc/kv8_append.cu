@@ -2,39 +2,118 @@
 //
 // Both move bytes (256 B in, 128 B out per bf16 row and the reverse) with a handful of
 // instructions per value, so HBM bounds them at length and latency at a few rows.
+#include <type_traits>
+
 #include "kv8_internal.cuh"
 
 namespace adamas {
 
-// A team of `team` warps owns one block of one (sequence, kv head) of K or of V: 8 rows
-// per warp (block size if smaller), held in registers between the maximum and the
-// rounding, so new rows are read once.  A lane holds elements 4l .. 4l+3 of a row (the
-// layout of the warp transform, which makes the key codes from the same registers).
-// Several teams share a CTA when blocks are small.
-constexpr int kRowsPerWarp = 8;
+// A team of warps owns one block of one (sequence, kv head) of K or of V.  A lane takes 16
+// bytes of a row per load (8 bf16 or 4 fp32 elements; 16 or 32 lanes to a row), kLoads loads
+// under way at once and held in registers between the maximum and the rounding, so new rows
+// are read once.  The maximum is taken on the raw bits (magnitudes of finite floats order as
+// integers).  Several teams share a CTA when blocks are small; a block of fewer rows than a
+// warp holds leaves lanes idle.
+constexpr int kLoads = 8;
+template <typename T>
+struct Vec {
+  static constexpr int kElems = 16 / int(sizeof(T));
+  static constexpr int kLanes = kD / kElems;                 // lanes to a row
+  static constexpr int kRowsPerLoad = 32 / kLanes;
+  static constexpr int kRows = kLoads * kRowsPerLoad;        // rows a warp holds
+};
 
-template <typename T, int FMT>
-__global__ void __launch_bounds__(1024) kv8_append_kernel(
+// Largest magnitude of a lane's elements as fp32 bits (0x7f800000 or more if one of them is not
+// finite), and the same without the non-finite ones.
+__device__ __forceinline__ uint32_t top_bits(const uint4& x, float) {
+  const uint32_t k = 0x7fffffffu;
+  return max(max(x.x & k, x.y & k), max(x.z & k, x.w & k));
+}
+__device__ __forceinline__ uint32_t top_bits(const uint4& x, __nv_bfloat16) {
+  const uint32_t k = 0x7fff7fffu;
+  const uint32_t m = __vmaxu2(__vmaxu2(x.x & k, x.y & k), __vmaxu2(x.z & k, x.w & k));
+  return max(m << 16, m & 0xffff0000u);
+}
+template <int E>
+__device__ __forceinline__ uint32_t top_finite(const float (&v)[E]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) m = fmaxf(m, finite_abs(v[i]));
+  return __float_as_uint(m);
+}
+
+__device__ __forceinline__ void elements(const uint4& x, float (&v)[4]) {
+  v[0] = __uint_as_float(x.x);
+  v[1] = __uint_as_float(x.y);
+  v[2] = __uint_as_float(x.z);
+  v[3] = __uint_as_float(x.w);
+}
+__device__ __forceinline__ void elements(const uint4& x, float (&v)[8]) {
+  bf16x2_to_f32(x.x, v[0], v[1]);
+  bf16x2_to_f32(x.y, v[2], v[3]);
+  bf16x2_to_f32(x.z, v[4], v[5]);
+  bf16x2_to_f32(x.w, v[6], v[7]);
+}
+
+// Key code of a row held E elements to a lane (element E l + i in lane l of the row): the
+// orthonormal Walsh-Hadamard transform in natural order, index bits below log2 E inside the lane,
+// the others across the row's lanes; then 2 bits per coordinate as warp_fwht_code gives them.
+template <int E>
+__device__ __forceinline__ uint32_t row_code(float (&v)[E], float t, float ratio, int lane) {
+#pragma unroll
+  for (int s = 1; s < E; s <<= 1)
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (!(i & s)) {
+        const float a = v[i], b = v[i | s];
+        v[i] = a + b;
+        v[i | s] = a - b;
+      }
+#pragma unroll
+  for (int s = 1; s < kD / E; s <<= 1) {
+    const float sg = (lane & s) ? -1.0f : 1.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) v[i] = fmaf(v[i], sg, __shfl_xor_sync(0xffffffffu, v[i], s));
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) v[i] *= 0.088388347648318440550f;   // 1 / sqrt(128)
+  if (ratio > 0.0f) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) m = fmaxf(m, fabsf(v[i]));
+#pragma unroll
+    for (int s = kD / E / 2; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+    t = ratio * m;
+  }
+  uint32_t code = 0;
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    code |= (uint32_t(v[i] >= -t) + uint32_t(v[i] >= 0.0f) + uint32_t(v[i] >= t)) << (2 * i);
+  return code;
+}
+
+// kCodes: the cache keeps key codes.
+template <typename T, int FMT, bool kCodes>
+__global__ void __launch_bounds__(256 * int(sizeof(T)), 4 / int(sizeof(T))) kv8_append_kernel(
     Kv8 c, const T* __restrict__ kn, const T* __restrict__ vn, int64_t n_new, int64_t sb,
     int64_t sh, int64_t sn, const int32_t* __restrict__ starts,
-    const int32_t* __restrict__ counts, float t, float ratio, int team, int blocks_per_seq,
-    int64_t items, uint32_t* err) {
-  __shared__ float warp_max[32];
-  using R = Raw4<T>;
+    const int32_t* __restrict__ counts, float t, float ratio, int team, uint32_t blocks_per_seq,
+    uint32_t items, uint32_t* err) {
+  using V = Vec<T>;
+  __shared__ uint32_t warp_top[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int teams = (blockDim.x >> 5) / team;
   const int wt = warp % team;
-  const int64_t item = int64_t(blockIdx.x) * teams + warp / team;
+  const uint32_t item = blockIdx.x * teams + warp / team;
   // kv heads innermost: neighbouring teams read neighbouring rows of token-major input
-  const int h = int(item % c.Hkv);
-  int64_t r = item / c.Hkv;
+  const int h = int(item % uint32_t(c.Hkv));
+  uint32_t r = item / uint32_t(c.Hkv);
   const bool is_v = r & 1;
   r >>= 1;
-  const int nth = int(r % blocks_per_seq);
   const int b = int(r / blocks_per_seq);
+  const int nth = int(r - b * blocks_per_seq);
   pdl_wait();
   pdl_trigger();
-  const int bs = 1 << c.bshift;
   bool active = item < items;
   int64_t start = 0, end = 0, first = 0, row0 = 0;
   if (active) {
@@ -56,74 +135,130 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(
       active = false;
     }
   }
+  // rows of the block, relative to `first`: new ones are [lo, hi), older ones lie below lo
+  const int bs = 1 << c.bshift;
+  const int lo = int(max(start - first, int64_t(0)));
+  const int hi = active ? int(min(end - first, int64_t(bs))) : 0;
+  const int mine = wt * V::kRows + lane / V::kLanes;         // this lane's first row
+  const int part = lane % V::kLanes;                         // its 16 bytes of a row
   float* const scale_at = (is_v ? c.vs : c.ks) + (row0 >> c.bshift);
-  const bool has_old = first < start;
-  const float old_s = active && has_old ? *scale_at : 0.0f;
-  const T* const src = (is_v ? vn : kn) + int64_t(b) * sb + int64_t(h) * sh;
-  const int rw = bs < kRowsPerWarp ? bs : kRowsPerWarp;
-  const int64_t p0 = first + wt * rw;                     // this warp's first position
-  typename R::type x[kRowsPerWarp];
-  float mx = 0.0f;
+  const float old_s = active && lo > 0 ? *scale_at : 0.0f;
+  const T* const src = (is_v ? vn : kn) + int64_t(b) * sb + int64_t(h) * sh +
+                       (first - start + mine) * sn + part * V::kElems;
+  const auto piece = [&](int u) {   // the u-th of this lane's 16-byte pieces
+    return __ldg(reinterpret_cast<const uint4*>(src + int64_t(u) * V::kRowsPerLoad * sn));
+  };
+  const auto is_new = [&](int u) {
+    const int row = mine + u * V::kRowsPerLoad;
+    return row >= lo && row < hi;
+  };
+  // a warp whose rows are all new needs no checks
+  const bool whole = wt * V::kRows >= lo && (wt + 1) * V::kRows <= hi;
+  uint4 x[kLoads];
+  if (whole) {
 #pragma unroll
-  for (int u = 0; u < kRowsPerWarp; ++u) {
-    const int64_t p = p0 + u;
-    if (active && u < rw && p >= start && p < end) {
-      x[u] = R::load(src + (p - start) * sn, lane);
-      float v[4];
-      R::decode(x[u], v);
-      mx = fmaxf(mx, fmaxf(fmaxf(finite_abs(v[0]), finite_abs(v[1])),
-                           fmaxf(finite_abs(v[2]), finite_abs(v[3]))));
+    for (int u = 0; u < kLoads; ++u) x[u] = piece(u);
+  } else {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      x[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (is_new(u)) x[u] = piece(u);
     }
   }
+  uint32_t top = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) warp_max[warp] = mx;
-  __syncthreads();   // also: every warp of the team has read the old scale
-  if (!active) return;
-  // the team's maximum: lane i takes warp i's
-  mx = lane < team ? warp_max[warp - wt + lane] : 0.0f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  const int e = scale_exponent<FMT>(mx);
+  for (int u = 0; u < kLoads; ++u) top = max(top, top_bits(x[u], T{}));
+  top = __reduce_max_sync(0xffffffffu, top);
+  if (top >= 0x7f800000u) {   // rare: the maximum again, without what is not finite
+    top = 0;
+#pragma unroll 1
+    for (int u = 0; u < kLoads; ++u) {
+      if (!is_new(u)) continue;
+      float v[V::kElems];
+      elements(piece(u), v);
+      top = max(top, top_finite(v));
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+  }
+  if (team > 1) {
+    if (lane == 0) warp_top[warp] = top;
+    __syncthreads();   // also: every warp of the team has read the old scale
+    top = __reduce_max_sync(0xffffffffu, lane < team ? warp_top[warp - wt + lane] : 0u);
+  }
+  if (hi == 0) return;
+  const int e = scale_exponent<FMT>(__uint_as_float(top));
   float s = pow2i(e), inv = pow2i(-e);
   uint8_t* const dst = (is_v ? c.v : c.k) + row0 * kD;
-  if (has_old) {
+  if (lo > 0) {
     if (old_s >= s) {
       s = old_s;
-      // 1/s: exact for the powers of two this kernel writes (never a smaller one than
-      // 2^-126, so the reciprocal is finite); a foreign scale's is rounded once
-      inv = 1.0f / s;
+      inv = 1.0f / s;   // exact for the powers of two that this kernel writes
     } else {
       // the present rows move to the larger scale: v * old rounded to the new grid
-#pragma unroll
-      for (int u = 0; u < kRowsPerWarp; ++u) {
-        const int64_t p = p0 + u;
-        if (u < rw && p < start) {
-          uint32_t* const w = reinterpret_cast<uint32_t*>(dst + (p - first) * kD) + lane;
-          float v[4];
-          unpack8<FMT>(*w, v);
-          *w = pack8<FMT>(v[0] * old_s * inv, v[1] * old_s * inv, v[2] * old_s * inv,
-                          v[3] * old_s * inv);
-        }
+      const int r1 = min(lo, (wt + 1) * V::kRows);
+#pragma unroll 1
+      for (int row = wt * V::kRows; row < r1; ++row) {
+        uint32_t* const w = reinterpret_cast<uint32_t*>(dst + row * kD) + lane;
+        float v[4];
+        unpack8<FMT>(*w, v);
+        *w = pack8<FMT>(v[0] * old_s * inv, v[1] * old_s * inv, v[2] * old_s * inv,
+                        v[3] * old_s * inv);
       }
     }
   }
   if (wt == 0 && lane == 0) *scale_at = s;
-  const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
+  const auto store = [&](int u, const float (&y)[V::kElems]) {
+    uint8_t* const o = dst + (mine + u * V::kRowsPerLoad) * kD + part * V::kElems;
+    if constexpr (V::kElems == 8)
+      *reinterpret_cast<uint2*>(o) = make_uint2(pack8<FMT>(y[0], y[1], y[2], y[3]),
+                                                pack8<FMT>(y[4], y[5], y[6], y[7]));
+    else
+      *reinterpret_cast<uint32_t*>(o) = pack8<FMT>(y[0], y[1], y[2], y[3]);
+  };
+  if ((__float_as_uint(s) & 0x7fffffu) != 0) {
+    // the block keeps a scale of another quantiser: divide
+#pragma unroll 1
+    for (int u = 0; u < kLoads; ++u) {
+      if (!is_new(u)) continue;
+      float v[V::kElems];
+      elements(piece(u), v);
 #pragma unroll
-  for (int u = 0; u < kRowsPerWarp; ++u) {
-    const int64_t p = p0 + u;
-    if (u < rw && p >= start && p < end) {
-      float v[4];
-      R::decode(x[u], v);
-      float y[4];
+      for (int i = 0; i < V::kElems; ++i) v[i] /= s;
+      store(u, v);
+    }
+  } else {
+    const auto round_rows = [&](auto all) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = pow2 ? v[i] * inv : v[i] / s;
-      reinterpret_cast<uint32_t*>(dst + (p - first) * kD)[lane] =
-          pack8<FMT>(y[0], y[1], y[2], y[3]);
-      if (!is_v && c.codes != nullptr)
-        c.codes[(row0 + (p - first)) * kCodeBytes + lane] =
-            static_cast<uint8_t>(warp_fwht_code(v, t, lane, ratio));
+      for (int u = 0; u < kLoads; ++u) {
+        if (!decltype(all)::value && !is_new(u)) continue;
+        float v[V::kElems];
+        elements(x[u], v);
+#pragma unroll
+        for (int i = 0; i < V::kElems; ++i) v[i] *= inv;
+        store(u, v);
+      }
+    };
+    if (whole) round_rows(std::true_type{});
+    else round_rows(std::false_type{});
+  }
+  if constexpr (kCodes) {
+    if (is_v) return;
+#pragma unroll 2
+    for (int u = 0; u < kLoads; ++u) {
+      // every lane of the warp takes part in the transform's exchanges
+      const bool there = is_new(u);
+      if (!__any_sync(0xffffffffu, there)) continue;
+      float v[V::kElems];
+      uint4 y = make_uint4(0u, 0u, 0u, 0u);
+      if (there) y = piece(u);   // in L1 or L2 since the first pass
+      elements(y, v);
+      const uint32_t code = row_code<V::kElems>(v, t, ratio, lane);
+      uint8_t* const o = c.codes + (row0 + mine + u * V::kRowsPerLoad) * kCodeBytes +
+                         part * (V::kElems / 4);
+      if (there) {
+        if constexpr (V::kElems == 8) *reinterpret_cast<uint16_t*>(o) = uint16_t(code);
+        else *o = uint8_t(code);
+      }
     }
   }
 }
@@ -134,14 +269,14 @@ static cudaError_t append_t(const Kv8& c, int fmt, const void* kn, const void* v
                             const int32_t* counts, float t, float ratio, uint32_t* err,
                             cudaStream_t stream) {
   const int bs = 1 << c.bshift;
-  const int team = bs < kRowsPerWarp ? 1 : bs / kRowsPerWarp;
+  const int team = bs <= Vec<T>::kRows ? 1 : bs / Vec<T>::kRows;
   const int warps = team > 8 ? team : 8;
   const int teams = warps / team;
   // the blocks n_new positions can touch when they start anywhere in a block
   const int64_t per_seq = (n_new + 2 * int64_t(bs) - 2) / bs;
   const int64_t items = int64_t(c.B) * c.Hkv * 2 * per_seq;
   const int64_t grid = (items + teams - 1) / teams;
-  if (per_seq > INT32_MAX || grid > INT32_MAX) return cudaErrorInvalidValue;
+  if (items + teams > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
   cfg.blockDim = dim3(unsigned(warps * 32));
@@ -154,10 +289,13 @@ static cudaError_t append_t(const Kv8& c, int fmt, const void* kn, const void* v
   const auto run = [&](auto kernel) {
     return cudaLaunchKernelEx(&cfg, kernel, c, static_cast<const T*>(kn),
                               static_cast<const T*>(vn), n_new, sb, sh, sn, starts, counts, t,
-                              ratio, team, int(per_seq), items, err);
+                              ratio, team, uint32_t(per_seq), uint32_t(items), err);
   };
-  return fmt == kFmtE4m3 ? run(kv8_append_kernel<T, kFmtE4m3>)
-                         : run(kv8_append_kernel<T, kFmtInt8>);
+  if (c.codes != nullptr)
+    return fmt == kFmtE4m3 ? run(kv8_append_kernel<T, kFmtE4m3, true>)
+                           : run(kv8_append_kernel<T, kFmtInt8, true>);
+  return fmt == kFmtE4m3 ? run(kv8_append_kernel<T, kFmtE4m3, false>)
+                         : run(kv8_append_kernel<T, kFmtInt8, false>);
 }
 
 cudaError_t launch_kv8_append(const Kv8& c, int fmt, const void* kn, const void* vn,
