@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(256 * int(sizeof(T)), 4 / int(sizeof(T))) kv8_
 #pragma unroll
   for (int u = 0; u < kLoads; ++u) top = max(top, top_bits(x[u], T{}));
   top = __reduce_max_sync(0xffffffffu, top);
-  if (top >= 0x7f800000u) {   // rare: the maximum again, without what is not finite
+  const bool odd = top >= 0x7f800000u;
+  if (odd) {   // rare: the maximum again, without what is not finite
     top = 0;
 #pragma unroll 1
     for (int u = 0; u < kLoads; ++u) {
@@ -207,24 +208,23 @@ __global__ void __launch_bounds__(256 * int(sizeof(T)), 4 / int(sizeof(T))) kv8_
     }
   }
   if (wt == 0 && lane == 0) *scale_at = s;
-  const auto store = [&](int u, const float (&y)[V::kElems]) {
+  const auto store = [&](int u, const uint32_t (&w)[V::kElems / 4]) {
     uint8_t* const o = dst + (mine + u * V::kRowsPerLoad) * kD + part * V::kElems;
-    if constexpr (V::kElems == 8)
-      *reinterpret_cast<uint2*>(o) = make_uint2(pack8<FMT>(y[0], y[1], y[2], y[3]),
-                                                pack8<FMT>(y[4], y[5], y[6], y[7]));
-    else
-      *reinterpret_cast<uint32_t*>(o) = pack8<FMT>(y[0], y[1], y[2], y[3]);
+    if constexpr (V::kElems == 8) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(o) = w[0];
   };
-  if ((__float_as_uint(s) & 0x7fffffu) != 0) {
-    // the block keeps a scale of another quantiser: divide
+  if (odd || (__float_as_uint(s) & 0x7fffffu) != 0) {
+    // not all elements are finite, or the block keeps a scale of another quantiser
 #pragma unroll 1
     for (int u = 0; u < kLoads; ++u) {
       if (!is_new(u)) continue;
       float v[V::kElems];
       elements(piece(u), v);
+      uint32_t w[V::kElems / 4];
 #pragma unroll
-      for (int i = 0; i < V::kElems; ++i) v[i] /= s;
-      store(u, v);
+      for (int i = 0; i < V::kElems / 4; ++i)
+        w[i] = pack8<FMT>(v[4 * i] / s, v[4 * i + 1] / s, v[4 * i + 2] / s, v[4 * i + 3] / s);
+      store(u, w);
     }
   } else {
     const auto round_rows = [&](auto all) {
@@ -233,9 +233,11 @@ __global__ void __launch_bounds__(256 * int(sizeof(T)), 4 / int(sizeof(T))) kv8_
         if (!decltype(all)::value && !is_new(u)) continue;
         float v[V::kElems];
         elements(x[u], v);
+        uint32_t w[V::kElems / 4];
 #pragma unroll
-        for (int i = 0; i < V::kElems; ++i) v[i] *= inv;
-        store(u, v);
+        for (int i = 0; i < V::kElems / 4; ++i)
+          w[i] = pack8_scaled<FMT>(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], inv);
+        store(u, w);
       }
     };
     if (whole) round_rows(std::true_type{});
@@ -337,13 +339,14 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(
     T* __restrict__ vo, uint32_t* err) {
   pdl_wait();
   pdl_trigger();
-  const int64_t unit = blockIdx.x / tiles;
-  const int64_t i0 = int64_t(blockIdx.x % tiles) * kReadRows;
-  const int b = int(unit / c.Hkv), h = int(unit % c.Hkv);
+  const uint32_t unit = blockIdx.x / uint32_t(tiles);
+  const int64_t i0 = int64_t(blockIdx.x - unit * tiles) * kReadRows;
+  const int b = int(unit / uint32_t(c.Hkv)), h = int(unit - b * c.Hkv);
   const uint8_t* const src = blockIdx.y ? c.v : c.k;
   const float* const sc = blockIdx.y ? c.vs : c.ks;
-  T* const dst = (blockIdx.y ? vo : ko) + unit * n * kD;
+  T* const dst = (blockIdx.y ? vo : ko) + int64_t(unit) * n * kD;
   const int64_t start = starts[b];
+  const UnitRows rows(c, b, h);
   const int piece = threadIdx.x & 7;
   uint4 w[kReadPer];
   float s[kReadPer];
@@ -355,7 +358,7 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(
     s[u] = -1.0f;                                             // no such row: zeros
     if (i < n) {
       const int64_t p = start + i;
-      const int64_t row = p >= 0 && p < c.Lmax ? kv8_row(c, b, h, p) : -1;
+      const int64_t row = p >= 0 && p < c.Lmax ? rows.row(int(p)) : -1;
       if (row >= 0) {
         w[u] = __ldg(reinterpret_cast<const uint4*>(src + row * kD) + piece);
         s[u] = __ldg(sc + (row >> c.bshift));

@@ -929,10 +929,11 @@ __global__ void __launch_bounds__(256) kv8_weights_kernel(
     const float* w_in, float* w_out, uint32_t* err) {
   pdl_wait();
   pdl_trigger();
-  const int64_t unit = blockIdx.x / tiles;
-  const int64_t j0 = int64_t(blockIdx.x % tiles) * (256 * kWPer) + threadIdx.x;
+  const uint32_t un = blockIdx.x / uint32_t(tiles);
+  const int64_t unit = un;
+  const int64_t j0 = int64_t(blockIdx.x - un * tiles) * (256 * kWPer) + threadIdx.x;
   const int64_t len =
-      seq_lens == nullptr ? Lmax : checked_len(seq_lens[unit / Hkv], Lmax, err, false);
+      seq_lens == nullptr ? Lmax : checked_len(seq_lens[un / uint32_t(Hkv)], Lmax, err, false);
   // the heads' weights are summed first: the (larger) running sum is rounded once
   float in[kWPer], s[kWPer];
 #pragma unroll
@@ -970,8 +971,9 @@ __global__ void __launch_bounds__(512) kv8_sparse_weights_kernel(
   extern __shared__ float sum[];
   pdl_wait();
   pdl_trigger();
-  const int64_t unit = blockIdx.x / slices;                     // (b, kv head)
-  const int64_t base = int64_t(blockIdx.x % slices) * kSlice;
+  const uint32_t un = blockIdx.x / uint32_t(slices);
+  const int64_t unit = un;                                      // (b, kv head)
+  const int64_t base = int64_t(blockIdx.x - un * slices) * kSlice;
   const int n = int(min(int64_t(kSlice), Lmax - base));
   for (int i = threadIdx.x; i < n; i += 512) sum[i] = 0.0f;
   __syncthreads();

@@ -13,18 +13,21 @@ namespace cg = cooperative_groups;
 // One thread-block cluster per (batch, kv head).  Each CTA keeps its share of the weights
 // in shared memory (read once).  The threshold, the n-th largest weight, is found by a
 // radix search over the 32-bit order-preserving keys, 11 + 11 + 10 bits: every CTA
-// histograms the next digit of the keys that share the prefix found so far, reads its
-// peers' histograms from distributed shared memory and finds the digit.  Then every CTA
+// histograms the next digit of the keys that share the prefix found so far and sends its
+// sums of 64 bins to its peers; the 64 bins where the count is reached are then read from all
+// (reading whole histograms, 64 KB per CTA, took 2 us a step).  Then every CTA
 // counts what it keeps, learns its offset from its peers, and writes positions and weights
 // in order.  Protected positions (first `sink`, last `recent`) are kept besides.
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMaxShare = 49152;                     // weights per CTA (192 KiB)
+static_assert(kSelWarps == 32 && kBins == 64 * kSelWarps, "a warp sums 64 bins, a lane holds a warp's");
+constexpr int kMaxShare = 49152;                     // weights per CTA (192 KiB, + 12 KiB of masks)
 constexpr int kMaxCluster = 16;
 
 struct SelSmem {
   uint32_t hist[2][kBins];
+  uint32_t coarse[3][kMaxCluster][kSelWarps];        // per search step: every CTA's sums of 64 bins
   uint32_t warp_a[kSelWarps], warp_b[kSelWarps];
   uint32_t kept, ties;                               // this CTA's counts (read by peers)
   uint32_t digit, above;                             // result of a search step
@@ -45,13 +48,16 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
   extern __shared__ __align__(16) uint8_t sel_raw[];
   SelSmem& sm = *reinterpret_cast<SelSmem*>(sel_raw);
   float* const val = reinterpret_cast<float*>(sel_raw + sizeof(SelSmem));
+  uint2* const masks = reinterpret_cast<uint2*>(val + share);   // per 32 positions: stay, tie
   const cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = blockIdx.x % cs;
-  const int64_t unit = blockIdx.x / cs;
+  const uint32_t chunk = blockIdx.x / uint32_t(cs);
+  const int rank = int(blockIdx.x - chunk * cs);
+  const int64_t unit = chunk;
   pdl_wait();
   pdl_trigger();
-  const int len = int(checked_len(seq_lens[unit / Hkv], Lmax, err, rank == 0 && tid == 0));
+  cluster.barrier_arrive();
+  const int len = int(checked_len(seq_lens[chunk / uint32_t(Hkv)], Lmax, err, rank == 0 && tid == 0));
   const int lo = min(len, rank * share), n = min(len, lo + share) - lo;
   const float* const w = w_in + unit * Lmax + lo;
   int32_t* const out = keep + unit * int64_t(budget);
@@ -78,42 +84,59 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
         if (pass == 0 || (key >> shift) == prefix)
           atomicAdd(&hist[(key >> below) & ((1u << bits) - 1u)], 1u);
       }
-      cluster.sync();
-      // all CTAs sum the cluster's histograms, four bins per thread, from the top bin down
-      const int bin0 = kBins - 4 * (tid + 1);
-      uint4 c = make_uint4(0u, 0u, 0u, 0u);
-      for (int r = 0; r < cs; ++r) {
-        const uint4 y = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(hist, r) + bin0);
-        c.x += y.x;
-        c.y += y.y;
-        c.z += y.z;
-        c.w += y.w;
-      }
-      const uint32_t mine = c.x + c.y + c.z + c.w;
-      uint32_t inc = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      if (lane == 31) sm.warp_a[warp] = inc;
-      // the other buffer was last read before this pass's cluster barrier
-      for (int i = tid; i < kBins; i += kSelThreads) sm.hist[(pass + 1) & 1][i] = 0u;
       __syncthreads();
-      uint32_t before = inc - mine;
-      for (int x = 0; x < warp; ++x) before += sm.warp_a[x];
-      if (before < need && before + mine >= need) {   // one thread
-        uint32_t a = before;
-        const uint32_t v[4] = {c.w, c.z, c.y, c.x};
-        int d = bin0 + 3;
+      // warp w sums bins 64 w .. + 63 and sends the sum to every CTA of the unit
+      const uint2 two = reinterpret_cast<const uint2*>(hist)[tid];
+      const uint32_t sum = __reduce_add_sync(0xffffffffu, two.x + two.y);
+      if (pass == 0) cluster.barrier_wait();   // every CTA of the cluster has started
+      if (lane < cs) cluster.map_shared_rank(&sm, lane)->coarse[pass][rank][warp] = sum;
+      cluster.sync();
+      if (warp == 0) {
+        // lane l: the unit's sum of chunk 31 - l; the chunk where the count from the top
+        // reaches `need`
+        uint32_t c = 0;
+        for (int r = 0; r < cs; ++r) c += sm.coarse[pass][r][31 - lane];
+        uint32_t inc = c;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (a + v[j] >= need) break;
-          a += v[j];
-          --d;
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
         }
-        sm.digit = uint32_t(d);
-        sm.above = a;
+        const int l = __ffs(__ballot_sync(0xffffffffu, inc >= need)) - 1;
+        const uint32_t above = __shfl_sync(0xffffffffu, inc - c, l);
+        // that chunk's bins, two per lane from the top, from all CTAs
+        const int bin0 = 64 * (31 - l) + 62 - 2 * lane;
+        uint2 b = make_uint2(0u, 0u);
+        for (int r0 = 0; r0 < cs; r0 += 8) {
+          uint2 y[8];   // requested together: a read of a peer's memory takes about 0.3 us
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            y[r] = make_uint2(0u, 0u);
+            if (r0 + r < cs)
+              y[r] = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(hist, r0 + r) + bin0);
+          }
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            b.x += y[r].x;
+            b.y += y[r].y;
+          }
+        }
+        uint32_t in2 = b.x + b.y;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, in2, o);
+          if (lane >= o) in2 += y;
+        }
+        in2 += above;
+        const uint32_t before = in2 - b.x - b.y;
+        if (before < need && in2 >= need) {   // one lane
+          const bool second = before + b.y < need;
+          sm.digit = uint32_t(bin0 + (second ? 0 : 1));
+          sm.above = second ? before + b.y : before;
+        }
+      } else {
+        // the other buffer was last read before this step's cluster barrier
+        for (int i = tid - 32; i < kBins; i += kSelThreads - 32) sm.hist[(pass + 1) & 1][i] = 0u;
       }
       __syncthreads();
       prefix = (prefix << bits) | sm.digit;
@@ -123,6 +146,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
     }
     thr = prefix;
     ties = need;
+  } else {
+    cluster.barrier_wait();
   }
   // which positions of this share stay: 0 no, 1 yes, 2 a tie at the threshold
   const auto state = [&](int i) -> int {
@@ -137,53 +162,58 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
   const int per = (groups + kSelWarps - 1) / kSelWarps;
   const int g0 = min(groups, warp * per), g1 = min(groups, g0 + per);
   uint32_t cnt = 0, tie = 0;
+#pragma unroll 4
   for (int g = g0; g < g1; ++g) {
     const int i = 32 * g + lane;
     const int s = i < n ? state(i) : 0;
-    cnt += __popc(__ballot_sync(0xffffffffu, s == 1));
-    tie += __popc(__ballot_sync(0xffffffffu, s == 2));
+    const uint32_t yes = __ballot_sync(0xffffffffu, s == 1), eq = __ballot_sync(0xffffffffu, s == 2);
+    if (lane == 0) masks[g] = make_uint2(yes, eq);
+    cnt += __popc(yes);
+    tie += __popc(eq);
   }
   if (lane == 0) {
     sm.warp_a[warp] = cnt;
     sm.warp_b[warp] = tie;
   }
   __syncthreads();
-  if (tid == 0) {
-    uint32_t a = 0, b = 0;
-    for (int x = 0; x < kSelWarps; ++x) {
-      a += sm.warp_a[x];
-      b += sm.warp_b[x];
+  const uint32_t wa = sm.warp_a[lane], wb = sm.warp_b[lane];   // one warp per lane
+  if (warp == 0) {
+    const uint32_t a = __reduce_add_sync(0xffffffffu, wa), b = __reduce_add_sync(0xffffffffu, wb);
+    if (lane == 0) {
+      sm.kept = a;
+      sm.ties = b;
     }
-    sm.kept = a;
-    sm.ties = b;
   }
   cluster.sync();   // counts are out; also: every CTA of the unit has read its weights
-  uint32_t ties_before = 0, at = 0;
-  for (int r = 0; r < rank; ++r) {
-    const SelSmem* const p = cluster.map_shared_rank(&sm, r);
-    ties_before += p->ties;
-    at += p->kept;
+  uint32_t at = 0, ties_before = 0;
+  if (lane < rank) {   // rank < 16
+    const SelSmem* const p = cluster.map_shared_rank(&sm, lane);
+    at = p->kept;
+    ties_before = p->ties;
   }
-  for (int x = 0; x < warp; ++x) {
-    at += sm.warp_a[x];
-    ties_before += sm.warp_b[x];
+  if (lane < warp) {
+    at += wa;
+    ties_before += wb;
   }
+  at = __reduce_add_sync(0xffffffffu, at);
+  ties_before = __reduce_add_sync(0xffffffffu, ties_before);
   at += min(ties_before, ties);
   float* const wo = w_out != nullptr ? w_out + unit * Lmax_out : nullptr;
+  const uint32_t lt = (1u << lane) - 1u;
+#pragma unroll 4
   for (int g = g0; g < g1; ++g) {
-    const int i = 32 * g + lane;
-    const int s = i < n ? state(i) : 0;
-    const uint32_t lt = (1u << lane) - 1u;
-    const uint32_t tmask = __ballot_sync(0xffffffffu, s == 2);
-    const bool stay = s == 1 || (s == 2 && ties_before + __popc(tmask & lt) < ties);
-    const uint32_t kmask = __ballot_sync(0xffffffffu, stay);
+    const uint2 m = masks[g];
+    // ties are taken in order while there is room
+    const uint32_t room = ties > ties_before ? ties - ties_before : 0u;
+    const bool stay = (m.x >> lane & 1u) || ((m.y >> lane & 1u) && uint32_t(__popc(m.y & lt)) < room);
+    const uint32_t before = __popc(m.x & lt) + min(uint32_t(__popc(m.y & lt)), room);
     if (stay) {
-      const uint32_t o = at + __popc(kmask & lt);
-      out[o] = lo + i;
-      if (wo != nullptr) wo[o] = val[i];
+      const int i = 32 * g + lane;
+      out[at + before] = lo + i;
+      if (wo != nullptr) wo[at + before] = val[i];
     }
-    at += __popc(kmask);
-    ties_before += __popc(tmask);
+    at += __popc(m.x) + min(uint32_t(__popc(m.y)), room);
+    ties_before += __popc(m.y);
   }
   // the rest of the list, and the weights the move leaves behind
   const int kept = min(len, budget);
@@ -196,75 +226,69 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
 }
 
 // ----------------------------------------------------------------------- moving
-// Row i of a unit comes from row keep[i] >= i (the list ascends), so moving rows down is
-// safe in place if a round's rows [i, i + c) are all read, by every CTA that works on the
-// unit, before any row below i + c is overwritten: later rounds read rows at or above
-// i + c only.  One cluster works on one unit's K, V or codes; a round is cluster size x kMoveRows rows, held
-// in registers across the cluster barrier, and the next round's rows are requested before
-// this round's are written.
+// Row i of a unit comes from row keep[i] >= i (the list ascends).  Into another cache every
+// chunk of rows is a CTA's own work.  In place one cluster works on one unit's K, V or
+// codes in rounds of (cluster size) chunks, kept in registers across the cluster's barrier: when
+// rows [i, i + c) are written, every row below i + c has been read by every CTA that needs it, and
+// later rounds read rows at or above i + c only; so the next round is requested before this one's
+// barrier.
 constexpr int kMoveThreads = 512;
-constexpr int kMoveRows = 256;                       // 8-bit rows per CTA and round
-constexpr int kMovePer = kMoveRows * 8 / kMoveThreads;   // 16-byte pieces per thread: 4
+// A thread holds a quarter of a row (32 bytes; what is done per row, its address, scale and ratio,
+// is then done four times, not eight as with 16 bytes: 133 -> MOVE_US us for 16 x 8 units at 16K).
+// Rows per thread: in place every round costs a cluster barrier, so it takes more rows.  Into
+// another cache a CTA is as small as a block allows (at least 64 rows), so that few warps wait at
+// its barrier.
+constexpr int move_per(bool in_place) { return in_place ? 4 : 2; }
+inline int move_threads(bool in_place, int bshift) {
+  return in_place ? kMoveThreads : (2 << bshift) > 128 ? 2 << bshift : 128;
+}
 
+template <int kPer>
 struct Round {
-  uint4 w[kMovePer];
-  float s[kMovePer];          // -1: no row
+  uint4 w[kPer][2];
+  float s[kPer];              // -1: no row
+  uint32_t stays;             // bit u: row u comes from its own place
 };
 
-template <int FMT>
-__device__ __forceinline__ uint32_t largest_byte(uint32_t w) {
-  // magnitudes of four bytes, as bytes; an e4m3 NaN does not count
-  if constexpr (FMT == kFmtE4m3) {
-    w &= 0x7f7f7f7fu;
-    return w & ~__vcmpeq4(w, 0x7f7f7f7fu);
-  } else {
-    return __vabsss4(w);
-  }
-}
-
-// the magnitude a byte stands for
-template <int FMT>
-__device__ __forceinline__ float magnitude(uint32_t byte) {
-  float v[4];
-  unpack8<FMT>(byte, v);
-  return v[0];
-}
-
-// blockIdx.x = ((unit * parts) + part) * cs + rank; part 0: K, 1: V, 2: codes.
-template <int FMT>
-__global__ void __launch_bounds__(kMoveThreads) kv8_move_kernel(
+// blockIdx.x = (unit * parts + part) * cs + rank; part 0: K, 1: V, 2: codes.  In place: cs CTAs
+// (one cluster) per unit and part, each taking every cs-th chunk; else cs chunks.
+template <int FMT, bool kInPlace>
+__global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) kv8_move_kernel(
     Kv8 src, Kv8 dst, const int32_t* __restrict__ keep, int n_keep,
-    const int32_t* seq_lens, int32_t* lens_out, int parts, int cs, bool in_place,
-    uint32_t* err) {
-  __shared__ uint32_t top[kMoveRows];                // largest value per block of the round
-  __shared__ uint32_t same[kMoveRows];               // rows of the block that stay in place
-  const cg::cluster_group cluster = cg::this_cluster();
+    const int32_t* seq_lens, int32_t* lens_out, int parts, int cs, uint32_t* err) {
+  constexpr int kMovePer = move_per(kInPlace), kMaxRows = kMovePer * kMoveThreads / 4;
+  const int threads = blockDim.x, rows = kMovePer * threads / 4;   // rows per CTA and round
+  __shared__ uint32_t top[2][kMaxRows];              // largest value per block of a round
+  __shared__ uint32_t same[kInPlace ? 2 : 1][kMaxRows];   // rows of the block that stay in place
   const int tid = threadIdx.x;
-  const int rank = blockIdx.x % cs;
-  const int part = (blockIdx.x / cs) % parts;
-  const int64_t unit = blockIdx.x / (cs * parts);
-  const int b = int(unit / src.Hkv), h = int(unit % src.Hkv);
+  const uint32_t chunk = blockIdx.x / uint32_t(cs);
+  const int rank = int(blockIdx.x - chunk * cs);
+  const uint32_t unit = chunk / uint32_t(parts);
+  const int part = int(chunk - unit * parts);
+  const int b = int(unit / uint32_t(src.Hkv)), h = int(unit - b * src.Hkv);
   pdl_wait();
   pdl_trigger();
   const int n = min(int(checked_len(seq_lens[b], src.Lmax, err, false)), n_keep);
   // every CTA that reads seq_lens[b] takes its minimum with n_keep, so it does not matter
   // whether it sees the old length or this
   if (lens_out != nullptr && h == 0 && part == 0 && rank == 0 && tid == 0) lens_out[b] = n;
-  const int32_t* const list = keep + unit * int64_t(n_keep);
+  const int32_t* const list = keep + int64_t(unit) * n_keep;
+  const UnitRows from_rows(src, b, h), to_rows(dst, b, h);
   if (part == 2) {
     // codes: rows of 32 bytes, two pieces each
-    constexpr int kRows = kMoveThreads * kMovePer / 2;
-    for (int i0 = 0; i0 < n; i0 += kRows * cs) {
-      uint4 w[kMovePer];
-      int64_t to[kMovePer];
+    constexpr int kCodePer = 4;
+    const int per_cta = threads * kCodePer / 2;
+    for (int i0 = 0; i0 < n; i0 += per_cta * cs) {
+      uint4 w[kCodePer];
+      int64_t to[kCodePer];
 #pragma unroll
-      for (int u = 0; u < kMovePer; ++u) {
-        const int i = i0 + rank * kRows + (u * kMoveThreads + tid) / 2;
+      for (int u = 0; u < kCodePer; ++u) {
+        const int i = i0 + rank * per_cta + (u * threads + tid) / 2;
         to[u] = -1;
         if (i < n) {
           const int p = list[i];
-          const int64_t from = p >= 0 && p < src.Lmax ? kv8_row(src, b, h, p) : -1;
-          const int64_t at = kv8_row(dst, b, h, i);
+          const int64_t from = p >= 0 && p < src.Lmax ? from_rows.row(p) : -1;
+          const int64_t at = to_rows.row(i);
           if (from >= 0 && at >= 0) {
             w[u] = *(reinterpret_cast<const uint4*>(src.codes + from * kCodeBytes) + (tid & 1));
             to[u] = at;
@@ -273,93 +297,144 @@ __global__ void __launch_bounds__(kMoveThreads) kv8_move_kernel(
           }
         }
       }
-      if (in_place) cluster.sync();
+      if (kInPlace) cg::this_cluster().sync();
 #pragma unroll
-      for (int u = 0; u < kMovePer; ++u)
+      for (int u = 0; u < kCodePer; ++u)
         if (to[u] >= 0)
           *(reinterpret_cast<uint4*>(dst.codes + to[u] * kCodeBytes) + (tid & 1)) = w[u];
     }
     return;
   }
+  if (!kInPlace && rank * rows >= n) return;
   const uint8_t* const from8 = part ? src.v : src.k;
   const float* const from_s = part ? src.vs : src.ks;
   uint8_t* const to8 = part ? dst.v : dst.k;
   float* const to_s = part ? dst.vs : dst.ks;
-  const int piece = tid & 7;
+  const int piece = tid & 3;
   const int bs = 1 << dst.bshift;
-  const auto load = [&](int i0, Round& r) {
+  const auto load = [&](int i0, Round<kMovePer>& r) {
+    int p[kMovePer];
+    r.stays = 0;
 #pragma unroll
     for (int u = 0; u < kMovePer; ++u) {
-      const int i = i0 + u * (kMoveThreads / 8) + (tid >> 3);
+      const int i = i0 + u * (threads / 4) + (tid >> 2);
+      // entries from n on are not used: loaded without waiting for n
+      p[u] = i < n_keep ? list[i] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kMovePer; ++u) {
+      const int i = i0 + u * (threads / 4) + (tid >> 2);
       r.s[u] = -1.0f;
+      r.w[u][0] = r.w[u][1] = make_uint4(0u, 0u, 0u, 0u);
       if (i < n) {
-        const int p = list[i];
-        const int64_t row = p >= 0 && p < src.Lmax ? kv8_row(src, b, h, p) : -1;
+        const int64_t row = p[u] >= 0 && p[u] < src.Lmax ? from_rows.row(p[u]) : -1;
         if (row >= 0) {
-          r.w[u] = *(reinterpret_cast<const uint4*>(from8 + row * kD) + piece);
+          const uint4* const p4 = reinterpret_cast<const uint4*>(from8 + row * kD) + piece;
+          r.w[u][0] = p4[0];
+          r.w[u][1] = p4[4];
           r.s[u] = from_s[row >> src.bshift];
+          if (kInPlace && p[u] == i) r.stays |= 1u << u;
         } else {
           atomicOr(err, kErrInput);
         }
       }
     }
   };
-  Round cur, nxt;
-  const int stride = kMoveRows * cs;
-  load(rank * kMoveRows, cur);
-  for (int i0 = rank * kMoveRows; i0 - rank * kMoveRows < n; i0 += stride) {
+  Round<kMovePer> cur, nxt;
+  const int stride = rows * cs;
+  int buf = 0;
+  load(rank * rows, cur);
+  for (int i = tid; i < rows; i += threads) {
+    top[0][i] = 0u;
+    if (kInPlace) same[0][i] = 0u;
+  }
+  __syncthreads();
+  for (int i0 = rank * rows; i0 - rank * rows < n; i0 += stride, buf ^= 1) {
     // the largest magnitude of every block of this CTA's rows
-    for (int i = tid; i < kMoveRows; i += kMoveThreads) top[i] = same[i] = 0u;
-    __syncthreads();
 #pragma unroll
     for (int u = 0; u < kMovePer; ++u) {
-      const int r = u * (kMoveThreads / 8) + (tid >> 3);
-      uint32_t m = 0;
-      if (cur.s[u] != -1.0f) {
-        m = __vmaxu4(__vmaxu4(largest_byte<FMT>(cur.w[u].x), largest_byte<FMT>(cur.w[u].y)),
-                     __vmaxu4(largest_byte<FMT>(cur.w[u].z), largest_byte<FMT>(cur.w[u].w)));
-        m = max(max(m & 0xffu, (m >> 8) & 0xffu), max((m >> 16) & 0xffu, m >> 24));
-      }
+      const int r = u * (threads / 4) + (tid >> 2);
+      __half2 m2 = __float2half2_rn(0.0f);
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (piece == 0 && cur.s[u] != -1.0f) {
-        atomicMax(&top[r >> dst.bshift], __float_as_uint(finite_abs(magnitude<FMT>(m) * cur.s[u])));
-        if (in_place && list[i0 + r] == i0 + r) atomicAdd(&same[r >> dst.bshift], 1u);
+      for (int j = 0; j < 2; ++j) {
+        m2 = max_magnitude<FMT>(cur.w[u][j].x, m2);
+        m2 = max_magnitude<FMT>(cur.w[u][j].y, m2);
+        m2 = max_magnitude<FMT>(cur.w[u][j].z, m2);
+        m2 = max_magnitude<FMT>(cur.w[u][j].w, m2);
       }
+      const float m = __half2float(__hmax(__low2half(m2), __high2half(m2)));
+      uint32_t v = cur.s[u] != -1.0f ? __float_as_uint(finite_abs(m * cur.s[u])) : 0u;
+      if (bs >= 8) {
+        // the warp's eight rows lie in one block
+        v = __reduce_max_sync(0xffffffffu, v);
+        if ((tid & 31) == 0) atomicMax(&top[buf][r >> dst.bshift], v);
+      } else {
+        atomicMax(&top[buf][r >> dst.bshift], v);
+      }
+      if (kInPlace && piece == 0 && (cur.stays >> u & 1u))
+        atomicAdd(&same[kInPlace ? buf : 0][r >> dst.bshift], 1u);
     }
-    if (i0 + stride - rank * kMoveRows < n) load(i0 + stride, nxt);
-    if (in_place) cluster.sync();   // all rows (and scales) of this round have been read
+    const bool more = kInPlace && i0 - rank * rows + stride < n;
+    if (more) load(i0 + stride, nxt);
+    if (kInPlace) cg::this_cluster().sync();   // this round's rows and scales have been read
     else __syncthreads();
+    if (more)
+      for (int i = tid; i < rows; i += threads) {
+        top[buf ^ 1][i] = 0u;
+        same[kInPlace ? buf ^ 1 : 0][i] = 0u;
+      }
 #pragma unroll
     for (int u = 0; u < kMovePer; ++u) {
-      const int r = u * (kMoveThreads / 8) + (tid >> 3);
+      const int r = u * (threads / 4) + (tid >> 2);
       const int i = i0 + r;
       if (cur.s[u] == -1.0f) continue;
       // a block whose rows all stay keeps its bytes and its scale
       const int first = i >> dst.bshift << dst.bshift;
-      if (in_place && same[r >> dst.bshift] == uint32_t(min(bs, n - first))) continue;
-      const int64_t at = kv8_row(dst, b, h, i);
+      if (kInPlace && same[kInPlace ? buf : 0][r >> dst.bshift] == uint32_t(min(bs, n - first)))
+        continue;
+      const int64_t at = to_rows.row(i);
       if (at < 0) {
         atomicOr(err, kErrInput);
         continue;
       }
-      const int e = scale_exponent<FMT>(__uint_as_float(top[r >> dst.bshift]));
+      bool odd_ratio = false;
+      const int e = scale_exponent<FMT>(__uint_as_float(top[buf][r >> dst.bshift]));
       const float s = pow2i(e);
       if (piece == 0 && i == first) to_s[at >> dst.bshift] = s;
-      uint32_t w[4] = {cur.w[u].x, cur.w[u].y, cur.w[u].z, cur.w[u].w};
+      uint32_t w[8] = {cur.w[u][0].x, cur.w[u][0].y, cur.w[u][0].z, cur.w[u][0].w,
+                       cur.w[u][1].x, cur.w[u][1].y, cur.w[u][1].z, cur.w[u][1].w};
       if (cur.s[u] != s) {
-        const float inv = pow2i(-e);
+        const float ratio = cur.s[u] * pow2i(-e);   // exact, e being a power of two's exponent
+        if ((__float_as_uint(ratio) & 0x807fffffu) == 0 && ratio >= 0x1p-14f && ratio <= 0x1p14f) {
+          const __half2 r2 = __float2half2_rn(ratio);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float v[4];
-          unpack8<FMT>(w[j], v);
-          w[j] = pack8<FMT>(v[0] * cur.s[u] * inv, v[1] * cur.s[u] * inv, v[2] * cur.s[u] * inv,
-                            v[3] * cur.s[u] * inv);
+          for (int j = 0; j < 8; ++j) w[j] = rescale8<FMT>(w[j], r2);
+        } else {
+          odd_ratio = true;
         }
       }
-      *(reinterpret_cast<uint4*>(to8 + at * kD) + piece) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (odd_ratio) {
+        // a scale of another quantiser, or one far from the new one
+#pragma unroll 1
+        for (int j = 0; j < 8; ++j) {
+          float v[4];
+          uint32_t x = w[0];
+#pragma unroll
+          for (int i = 1; i < 8; ++i) x = j == i ? w[i] : x;
+          unpack8<FMT>(x, v);
+          const float f = pow2i(-e);
+          reinterpret_cast<uint32_t*>(to8 + at * kD)[4 * piece + (j & 3) + 16 * (j >> 2)] =
+              pack8<FMT>(v[0] * cur.s[u] * f, v[1] * cur.s[u] * f, v[2] * cur.s[u] * f,
+                         v[3] * cur.s[u] * f);
+        }
+        continue;
+      }
+      uint4* const o = reinterpret_cast<uint4*>(to8 + at * kD) + piece;
+      o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      o[4] = make_uint4(w[4], w[5], w[6], w[7]);
     }
-    __syncthreads();   // top / same are free again
+    if (!kInPlace) return;
+    __syncthreads();   // the other buffers are clear, this one is read
     cur = nxt;
   }
 }
@@ -371,13 +446,14 @@ __global__ void __launch_bounds__(kMoveThreads) move_rows_kernel(
   constexpr int kPer = 8;
   const cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x;
-  const int rank = blockIdx.x % cs;
-  const int64_t unit = blockIdx.x / cs;
-  const int b = int(unit / lay.Hkv), h = int(unit % lay.Hkv);
+  const uint32_t unit = blockIdx.x / uint32_t(cs);
+  const int rank = int(blockIdx.x - unit * cs);
+  const int b = int(unit / uint32_t(lay.Hkv)), h = int(unit - b * lay.Hkv);
   pdl_wait();
   pdl_trigger();
   const int n = min(int(checked_len(seq_lens[b], lay.Lmax, err, rank == 0 && tid == 0)), n_keep);
-  const int32_t* const list = keep + unit * int64_t(n_keep);
+  const int32_t* const list = keep + int64_t(unit) * n_keep;
+  const UnitRows rows_of(lay, b, h);
   const int rows = (kMoveThreads * kPer) >> pshift;
   const int piece = tid & ((1 << pshift) - 1);
   for (int i0 = 0; i0 < n; i0 += rows * cs) {
@@ -389,8 +465,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_rows_kernel(
       to[u] = -1;
       if (i < n) {
         const int p = list[i];
-        const int64_t from = p >= 0 && p < lay.Lmax ? kv8_row(lay, b, h, p) : -1;
-        const int64_t at = kv8_row(lay, b, h, i);
+        const int64_t from = p >= 0 && p < lay.Lmax ? rows_of.row(p) : -1;
+        const int64_t at = rows_of.row(i);
         if (from >= 0 && at >= 0) {
           w[u] = src[(from << pshift) + piece];
           to[u] = at;
@@ -436,7 +512,7 @@ cudaError_t launch_evict_select(const float* w, int B, int Hkv, int64_t Lmax,
   static std::atomic<uint64_t> done{0};
   const cudaError_t e =
       allow_smem(reinterpret_cast<const void*>(evict_select_kernel),
-                 int(sizeof(SelSmem)) + kMaxShare * 4, done, true);
+                 int(sizeof(SelSmem)) + kMaxShare * 4 + kMaxShare / 4, done, true);
   if (e != cudaSuccess) return e;
   // shares of at least 4096 weights while the units leave SMs free, and of at most what
   // shared memory holds
@@ -451,7 +527,7 @@ cudaError_t launch_evict_select(const float* w, int B, int Hkv, int64_t Lmax,
   cluster_config(cfg, attr, cs);
   cfg.gridDim = dim3(unsigned(units * cs));
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = sizeof(SelSmem) + size_t(share) * 4;
+  cfg.dynamicSmemBytes = sizeof(SelSmem) + size_t(share) * 4 + size_t(share) / 4;
   cfg.stream = stream;
   return cudaLaunchKernelEx(&cfg, evict_select_kernel, w, Hkv, Lmax, seq_lens, budget, sink,
                             recent, keep, w_out, Lmax_out, cs, share, err);
@@ -462,20 +538,25 @@ cudaError_t launch_kv8_compact(const Kv8& src, const Kv8& dst, int fmt, const in
                                uint32_t* err, cudaStream_t stream) {
   const int parts = dst.codes != nullptr ? 3 : 2;
   const int64_t units = int64_t(src.B) * src.Hkv;
-  const int cs = move_cluster(n_keep, kMoveRows, units * parts);
+  const bool in_place = src.k == dst.k;
+  const int threads = move_threads(in_place, dst.bshift);
+  const int rows = move_per(in_place) * threads / 4;
+  const int64_t cs = in_place ? move_cluster(n_keep, rows, units * parts)
+                              : (int64_t(n_keep) + rows - 1) / rows;
   if (units * parts * cs > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  cluster_config(cfg, attr, cs);
+  cluster_config(cfg, attr, in_place ? int(cs) : 1);
   cfg.gridDim = dim3(unsigned(units * parts * cs));
-  cfg.blockDim = dim3(kMoveThreads);
+  cfg.blockDim = dim3(unsigned(threads));
   cfg.stream = stream;
-  const bool in_place = src.k == dst.k;
+  const auto run = [&](auto kernel) {
+    return cudaLaunchKernelEx(&cfg, kernel, src, dst, keep, n_keep, seq_lens, lens_out, parts,
+                              int(cs), err);
+  };
   if (fmt == kFmtE4m3)
-    return cudaLaunchKernelEx(&cfg, kv8_move_kernel<kFmtE4m3>, src, dst, keep, n_keep, seq_lens,
-                              lens_out, parts, cs, in_place, err);
-  return cudaLaunchKernelEx(&cfg, kv8_move_kernel<kFmtInt8>, src, dst, keep, n_keep, seq_lens,
-                            lens_out, parts, cs, in_place, err);
+    return in_place ? run(kv8_move_kernel<kFmtE4m3, true>) : run(kv8_move_kernel<kFmtE4m3, false>);
+  return in_place ? run(kv8_move_kernel<kFmtInt8, true>) : run(kv8_move_kernel<kFmtInt8, false>);
 }
 
 cudaError_t launch_compact_rows(const Kv8& lay, const void* src, void* dst, int row_bytes,

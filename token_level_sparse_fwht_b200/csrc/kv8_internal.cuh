@@ -38,6 +38,25 @@ __device__ __forceinline__ int64_t kv8_row(const Kv8& c, int b, int h, int64_t p
   return ((int64_t(page) * c.Hkv + h) << c.page_shift) + (pos & ((int64_t(1) << c.page_shift) - 1));
 }
 
+// The rows of one (b, kv head), for loops over its positions.
+struct UnitRows {
+  const int32_t* table;
+  int64_t base;      // contiguous: the row of position 0
+  int64_t pages;
+  int shift, hkv, h;
+  __device__ __forceinline__ UnitRows(const Kv8& c, int b, int head)
+      : table(c.table == nullptr ? nullptr : c.table + int64_t(b) * c.max_blocks),
+        base((int64_t(b) * c.Hkv + head) * c.Lmax), pages(c.num_pages), shift(c.page_shift),
+        hkv(c.Hkv), h(head) {}
+  // row of position pos (0 <= pos < Lmax), or -1 if its page id is out of range
+  __device__ __forceinline__ int64_t row(int pos) const {
+    if (table == nullptr) return base + pos;
+    const int page = table[pos >> shift];
+    if (page < 0 || page >= pages) return -1;
+    return ((int64_t(page) * hkv + h) << shift) + (pos & ((1 << shift) - 1));
+  }
+};
+
 // A sequence length clamped into [0, top]; one out of range is recorded.
 __device__ __forceinline__ int64_t checked_len(int len, int64_t top, uint32_t* err, bool report) {
   if (len < 0 || len > top) {
@@ -118,6 +137,54 @@ __device__ __forceinline__ void unpack8(uint32_t w, float v[4]) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
     v[2 * h] = f.x;
     v[2 * h + 1] = f.y;
+  }
+}
+
+// Four finite values times inv (a power of two that brings them into the format's range) to four
+// bytes, as pack8 would.  int8: adding 1.5 x 2^23 in the same fused multiply-add rounds to an integer
+// (ties to even) whose low byte is the answer.
+template <int FMT>
+__device__ __forceinline__ uint32_t pack8_scaled(float a, float b, float c, float d, float inv) {
+  if constexpr (FMT == kFmtE4m3) {
+    return pack8<FMT>(a * inv, b * inv, c * inv, d * inv);
+  } else {
+    const float k = 12582912.0f;
+    const uint32_t ab = __byte_perm(__float_as_uint(fmaf(a, inv, k)), __float_as_uint(fmaf(b, inv, k)), 0x0040);
+    const uint32_t cd = __byte_perm(__float_as_uint(fmaf(c, inv, k)), __float_as_uint(fmaf(d, inv, k)), 0x0040);
+    return __byte_perm(ab, cd, 0x5410);
+  }
+}
+
+// Largest magnitude among four bytes' values and m (both halves), NaN left out.
+template <int FMT>
+__device__ __forceinline__ __half2 max_magnitude(uint32_t w, __half2 m) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t x = half2_of<FMT>(w, h);
+    m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&x)));
+  }
+  return m;
+}
+
+// Four bytes times r (a power of two in [2^-14, 2^14], both halves of `ratio`), rounded to the
+// format; the results must be in its range.  In fp16: products of the formats' values with a power of
+// two are exact there (an e4m3 result below 2^-24 rounds to zero either way).  int8: adding 1536
+// in the fused multiply-add rounds to an integer (ties to even) whose low byte is the answer.
+template <int FMT>
+__device__ __forceinline__ uint32_t rescale8(uint32_t w, __half2 ratio) {
+  const uint32_t x0 = half2_of<FMT>(w, 0), x1 = half2_of<FMT>(w, 1);
+  if constexpr (FMT == kFmtE4m3) {
+    const __half2 y0 = __hmul2(*reinterpret_cast<const __half2*>(&x0), ratio);
+    const __half2 y1 = __hmul2(*reinterpret_cast<const __half2*>(&x1), ratio);
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(*reinterpret_cast<const uint32_t*>(&y0)));
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(*reinterpret_cast<const uint32_t*>(&y1)));
+    return uint32_t(lo) | (uint32_t(hi) << 16);
+  } else {
+    const __half2 k = __float2half2_rn(1536.0f);
+    const __half2 y0 = __hfma2(*reinterpret_cast<const __half2*>(&x0), ratio, k);
+    const __half2 y1 = __hfma2(*reinterpret_cast<const __half2*>(&x1), ratio, k);
+    return __byte_perm(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1), 0x6420);
   }
 }
 
