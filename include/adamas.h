@@ -487,7 +487,8 @@ adamas_status adamas_decode_plan_shared(int B, int Hq, int Hkv, int d, int64_t L
  * [num_pages][Hkv][page_size][d/4]; position p of sequence b is row p % page_size of
  * page block_table[b * max_blocks_per_seq + p / page_size], and Lmax is the longest
  * sequence (Lmax <= max_blocks_per_seq * page_size).  block_size is a power of two in
- * [1, 256]; contiguous caches need Lmax % block_size == 0.  A page that is written
+ * [1, 256]; contiguous caches need Lmax % block_size == 0.  A cache has at most 2^31 - 1 rows
+ * (B * Hkv * Lmax, or num_pages * Hkv * page_size; ADAMAS_ERR_UNSUPPORTED above).  A page that is written
  * (append, evict) must belong to one sequence.  codes may be NULL.  Alignment: 16
  * bytes for rows and codes, 4 for scales and integer arrays, 256 for workspaces.
  *

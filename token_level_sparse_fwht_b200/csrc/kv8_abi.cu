@@ -49,12 +49,14 @@ adamas_status check_layout(int B, int Hkv, int64_t Lmax, int page_size, int64_t 
   c.Lmax = Lmax;
   if (page_size == 0) {
     if (table != nullptr) return ADAMAS_ERR_INVALID_ARG;
-    return ADAMAS_OK;
+    return int64_t(B) * Hkv * Lmax <= INT32_MAX ? ADAMAS_OK : ADAMAS_ERR_UNSUPPORTED;
   }
   if (page_size < 0 || page_size > (1 << 20) || !pow2(page_size)) return ADAMAS_ERR_INVALID_ARG;
   if (num_pages < 1 || num_pages > INT32_MAX || max_blocks < 1 || table == nullptr ||
       !aligned(table, 4) || int64_t(max_blocks) * page_size < Lmax)
     return ADAMAS_ERR_INVALID_ARG;
+  if (num_pages > INT32_MAX / Hkv || num_pages * Hkv > INT32_MAX / page_size)
+    return ADAMAS_ERR_UNSUPPORTED;   // kernels index rows with 32 bits
   c.table = table;
   c.num_pages = num_pages;
   c.max_blocks = max_blocks;
@@ -106,11 +108,15 @@ adamas_status check_weights(const float* in, const float* out) {
 }
 
 // Workspace sizes also answer for arguments that no call accepts: 0.
+// A call's 256-key steps are counted in 32 bits.
+bool few_steps(int64_t units, int64_t n) { return units * ((n + 255) / 256) <= INT32_MAX / 2; }
+
 adamas_status check_attention_sizes(int B, int Hq, int Hkv, int d, int64_t n) {
   if (B <= 0 || n <= 0) return ADAMAS_ERR_INVALID_ARG;
   const adamas_status s = check_heads(Hq, Hkv);
   if (s != ADAMAS_OK) return s;
-  if (d != kD || int64_t(B) * Hkv > (1 << 24) || n > kMaxLen) return ADAMAS_ERR_UNSUPPORTED;
+  if (d != kD || int64_t(B) * Hkv > (1 << 24) || n > kMaxLen || !few_steps(int64_t(B) * Hq, n))
+    return ADAMAS_ERR_UNSUPPORTED;
   return ADAMAS_OK;
 }
 
@@ -124,6 +130,7 @@ adamas_status attention_common(const void* q, adamas_dtype dt, const adamas_kv8_
   if (s != ADAMAS_OK) return s;
   s = check_heads(Hq, c.Hkv);
   if (s != ADAMAS_OK) return s;
+  if (!few_steps(int64_t(c.B) * Hq, idx ? k : c.Lmax)) return ADAMAS_ERR_UNSUPPORTED;
   s = check_weights(w_in, w_out);
   if (s != ADAMAS_OK) return s;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(seq_lens, 4) || !aligned(idx, 4))

@@ -280,17 +280,17 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) kv8_move_kerne
     const int per_cta = threads * kCodePer / 2;
     for (int i0 = 0; i0 < n; i0 += per_cta * cs) {
       uint4 w[kCodePer];
-      int64_t to[kCodePer];
+      int to[kCodePer];
 #pragma unroll
       for (int u = 0; u < kCodePer; ++u) {
         const int i = i0 + rank * per_cta + (u * threads + tid) / 2;
         to[u] = -1;
         if (i < n) {
           const int p = list[i];
-          const int64_t from = p >= 0 && p < src.Lmax ? from_rows.row(p) : -1;
-          const int64_t at = to_rows.row(i);
+          const int from = p >= 0 && p < src.Lmax ? from_rows.row(p) : -1;
+          const int at = to_rows.row(i);
           if (from >= 0 && at >= 0) {
-            w[u] = *(reinterpret_cast<const uint4*>(src.codes + from * kCodeBytes) + (tid & 1));
+            w[u] = *(reinterpret_cast<const uint4*>(src.codes + int64_t(from) * kCodeBytes) + (tid & 1));
             to[u] = at;
           } else {
             atomicOr(err, kErrInput);
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) kv8_move_kerne
 #pragma unroll
       for (int u = 0; u < kCodePer; ++u)
         if (to[u] >= 0)
-          *(reinterpret_cast<uint4*>(dst.codes + to[u] * kCodeBytes) + (tid & 1)) = w[u];
+          *(reinterpret_cast<uint4*>(dst.codes + int64_t(to[u]) * kCodeBytes) + (tid & 1)) = w[u];
     }
     return;
   }
@@ -327,9 +327,9 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) kv8_move_kerne
       r.s[u] = -1.0f;
       r.w[u][0] = r.w[u][1] = make_uint4(0u, 0u, 0u, 0u);
       if (i < n) {
-        const int64_t row = p[u] >= 0 && p[u] < src.Lmax ? from_rows.row(p[u]) : -1;
+        const int row = p[u] >= 0 && p[u] < src.Lmax ? from_rows.row(p[u]) : -1;
         if (row >= 0) {
-          const uint4* const p4 = reinterpret_cast<const uint4*>(from8 + row * kD) + piece;
+          const uint4* const p4 = reinterpret_cast<const uint4*>(from8 + int64_t(row) * kD) + piece;
           r.w[u][0] = p4[0];
           r.w[u][1] = p4[4];
           r.s[u] = from_s[row >> src.bshift];
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) kv8_move_kerne
       const int first = i >> dst.bshift << dst.bshift;
       if (kInPlace && same[kInPlace ? buf : 0][r >> dst.bshift] == uint32_t(min(bs, n - first)))
         continue;
-      const int64_t at = to_rows.row(i);
+      const int at = to_rows.row(i);
       if (at < 0) {
         atomicOr(err, kErrInput);
         continue;
@@ -423,13 +423,13 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) kv8_move_kerne
           for (int i = 1; i < 8; ++i) x = j == i ? w[i] : x;
           unpack8<FMT>(x, v);
           const float f = pow2i(-e);
-          reinterpret_cast<uint32_t*>(to8 + at * kD)[4 * piece + (j & 3) + 16 * (j >> 2)] =
+          reinterpret_cast<uint32_t*>(to8 + int64_t(at) * kD)[4 * piece + (j & 3) + 16 * (j >> 2)] =
               pack8<FMT>(v[0] * cur.s[u] * f, v[1] * cur.s[u] * f, v[2] * cur.s[u] * f,
                          v[3] * cur.s[u] * f);
         }
         continue;
       }
-      uint4* const o = reinterpret_cast<uint4*>(to8 + at * kD) + piece;
+      uint4* const o = reinterpret_cast<uint4*>(to8 + int64_t(at) * kD) + piece;
       o[0] = make_uint4(w[0], w[1], w[2], w[3]);
       o[4] = make_uint4(w[4], w[5], w[6], w[7]);
     }
@@ -458,17 +458,17 @@ __global__ void __launch_bounds__(kMoveThreads) move_rows_kernel(
   const int piece = tid & ((1 << pshift) - 1);
   for (int i0 = 0; i0 < n; i0 += rows * cs) {
     uint4 w[kPer];
-    int64_t to[kPer];
+    int to[kPer];
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const int i = i0 + rank * rows + ((u * kMoveThreads + tid) >> pshift);
       to[u] = -1;
       if (i < n) {
         const int p = list[i];
-        const int64_t from = p >= 0 && p < lay.Lmax ? rows_of.row(p) : -1;
-        const int64_t at = rows_of.row(i);
+        const int from = p >= 0 && p < lay.Lmax ? rows_of.row(p) : -1;
+        const int at = rows_of.row(i);
         if (from >= 0 && at >= 0) {
-          w[u] = src[(from << pshift) + piece];
+          w[u] = src[(int64_t(from) << pshift) + piece];
           to[u] = at;
         } else {
           atomicOr(err, kErrInput);
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_rows_kernel(
     if (in_place) cluster.sync();
 #pragma unroll
     for (int u = 0; u < kPer; ++u)
-      if (to[u] >= 0) dst[(to[u] << pshift) + piece] = w[u];
+      if (to[u] >= 0) dst[(int64_t(to[u]) << pshift) + piece] = w[u];
   }
 }
 

@@ -38,22 +38,22 @@ __device__ __forceinline__ int64_t kv8_row(const Kv8& c, int b, int h, int64_t p
   return ((int64_t(page) * c.Hkv + h) << c.page_shift) + (pos & ((int64_t(1) << c.page_shift) - 1));
 }
 
-// The rows of one (b, kv head), for loops over its positions.
+// The rows of one (b, kv head), for loops over its positions.  (A buffer has fewer than 2^31 rows:
+// the entry points refuse others.)
 struct UnitRows {
   const int32_t* table;
-  int64_t base;      // contiguous: the row of position 0
-  int64_t pages;
-  int shift, hkv, h;
+  int base;      // contiguous: the row of position 0
+  int pages, shift, hkv, h;
   __device__ __forceinline__ UnitRows(const Kv8& c, int b, int head)
       : table(c.table == nullptr ? nullptr : c.table + int64_t(b) * c.max_blocks),
-        base((int64_t(b) * c.Hkv + head) * c.Lmax), pages(c.num_pages), shift(c.page_shift),
-        hkv(c.Hkv), h(head) {}
+        base(c.table == nullptr ? (b * c.Hkv + head) * int(c.Lmax) : 0), pages(int(c.num_pages)),
+        shift(c.page_shift), hkv(c.Hkv), h(head) {}
   // row of position pos (0 <= pos < Lmax), or -1 if its page id is out of range
-  __device__ __forceinline__ int64_t row(int pos) const {
+  __device__ __forceinline__ int row(int pos) const {
     if (table == nullptr) return base + pos;
-    const int page = table[pos >> shift];
+    const int page = __ldg(table + (pos >> shift));
     if (page < 0 || page >= pages) return -1;
-    return ((int64_t(page) * hkv + h) << shift) + (pos & ((1 << shift) - 1));
+    return ((page * hkv + h) << shift) + (pos & ((1 << shift) - 1));
   }
 };
 
@@ -104,6 +104,15 @@ __device__ __forceinline__ uint32_t pack8(float a, float b, float c, float d) {
   }
 }
 
+// Four int8 as biased bytes (v + 128).  Opaque to the compiler, which otherwise moves the operation
+// up to a conditional load of w (zeros ^ constant on the other path) and so waits for every load in
+// turn: adamas_kv8_read took 44 instead of 33 us for 32K rows of 8 heads.
+__device__ __forceinline__ uint32_t biased(uint32_t w) {
+  uint32_t x;
+  asm("xor.b32 %0, %1, 0x80808080;" : "=r"(x) : "r"(w));
+  return x;
+}
+
 // Bytes 2h and 2h + 1 of w as two exact fp16 values (the lower byte in the low half).
 // e4m3: one conversion.  int8: the biased byte u = v + 128 under an exponent byte 0x64
 // is 1024 + u; subtracting 1152 leaves v exactly.
@@ -122,7 +131,7 @@ __device__ __forceinline__ uint32_t half2_of(uint32_t w, int h) {
           : "=r"(r)
           : "r"(w));
   } else {
-    const uint32_t f = __byte_perm(w ^ 0x80808080u, 0x64646464u, h ? 0x4342u : 0x4140u);
+    const uint32_t f = __byte_perm(biased(w), 0x64646464u, h ? 0x4342u : 0x4140u);
     asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(f), "r"(0x64806480u));
   }
   return r;
@@ -152,6 +161,28 @@ __device__ __forceinline__ uint32_t pack8_scaled(float a, float b, float c, floa
     const uint32_t ab = __byte_perm(__float_as_uint(fmaf(a, inv, k)), __float_as_uint(fmaf(b, inv, k)), 0x0040);
     const uint32_t cd = __byte_perm(__float_as_uint(fmaf(c, inv, k)), __float_as_uint(fmaf(d, inv, k)), 0x0040);
     return __byte_perm(ab, cd, 0x5410);
+  }
+}
+
+// Four bytes times a scale (v * s rounded once).  int8: the biased byte in the last place of 2^23
+// is a float; for a power of two s its offset leaves in the same fused multiply-add, exactly.
+template <int FMT, bool kPow2>
+__device__ __forceinline__ void scaled8(uint32_t w, float s, float v[4]) {
+  if constexpr (FMT == kFmtE4m3) {
+    unpack8<FMT>(w, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] *= s;
+  } else {
+    const uint32_t x = biased(w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(__byte_perm(x, 0x4b000000u, 0x7440u | i));
+    if constexpr (kPow2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = fmaf(v[i], s, -8388736.0f * s);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = (v[i] - 8388736.0f) * s;
+    }
   }
 }
 
