@@ -108,8 +108,8 @@ adamas_status check_weights(const float* in, const float* out) {
 }
 
 // Workspace sizes also answer for arguments that no call accepts: 0.
-// A call's 256-key steps are counted in 32 bits.
-bool few_steps(int64_t units, int64_t n) { return units * ((n + 255) / 256) <= INT32_MAX / 2; }
+// A call's 128-key steps are counted in 32 bits.
+bool few_steps(int64_t units, int64_t n) { return units * ((n + 127) / 128) <= INT32_MAX / 2; }
 
 adamas_status check_attention_sizes(int B, int Hq, int Hkv, int d, int64_t n) {
   if (B <= 0 || n <= 0) return ADAMAS_ERR_INVALID_ARG;

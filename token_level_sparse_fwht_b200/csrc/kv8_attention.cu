@@ -26,15 +26,15 @@
 // parts of w for four heads (head rows repeated); with G <= 8 (NT = 2) each product is taken
 // twice, with the high and with the low parts.
 //
-// Layout of the work.  A step is 256 keys of a unit: 32 per warp, 8 warps.  The steps of all
-// units form one line that is cut evenly over the CTAs (lengths are read on the device),
-// so unequal sequences balance; a CTA's cut may hold the end of one unit, whole units and
+// Layout of the work.  A step is 128 keys of a unit: 32 per warp, 4 warps.  The steps of all
+// units form one line (with kUnitCost places more per unit, for what its start and its merge cost)
+// that is cut evenly over the CTAs; lengths are read on the device, so unequal sequences balance; a CTA's cut may hold the end of one unit, whole units and
 // the start of another.  Each lane loads the 16-byte pieces of K and V rows that its fragments
 // need straight into registers: a tile's K registers are refilled (with the next tile, of the next
 // unit if need be) as soon as its scores are formed, the V registers after its value product,
 // so 8 KB per warp stay under way through the rest of the work.  At a unit's end the warps'
-// states are merged; a unit cut between CTAs is merged from the partial results in the workspace,
-// in CTA order, by the last CTA to finish its part.
+// states are merged; a unit cut between CTAs leaves its parts in the workspace, and a second kernel,
+// which is launched early and waits, merges them in CTA order.
 //
 // kUni: 16 rows of a tile follow one another and share one scale (contiguous caches and pages
 // of at least 16 rows, blocks of at least 16 positions); otherwise (given positions, small
@@ -47,11 +47,13 @@ namespace adamas {
 
 namespace {
 
-constexpr int kWarps = 8;                        // one CTA per SM: up to 255 registers a thread
+constexpr int kWarps = 4;                        // two CTAs per SM: up to 255 registers a thread
+constexpr int kCtasPerSm = 2;
 constexpr int kThr = kWarps * 32;
 constexpr int kTile = 32;                        // keys per warp and step, in two halves of 16
 constexpr int kStep = kWarps * kTile;            // keys per step
-constexpr int kMaxParts = 160;                   // parts of a unit whose factors fit in shared memory
+constexpr int kUnitCost = 2;                     // steps that a unit's start and merge take as long as
+constexpr int kMaxParts = 512;                   // CTAs, and so parts of a unit
 constexpr float kWBias = 14.0f;                  // w is held times 2^14
 constexpr int kPart = 4 + kD;                    // floats of a partial: m, l, m2, 0, sums
 
@@ -59,11 +61,8 @@ constexpr int kPart = 4 + kD;                    // floats of a partial: m, l, m
 template <int NT>
 struct Smem {
   static constexpr int kSums = NT == 1 ? 16 : 32;   // values per lane when warps are merged
-  float sums[kWarps][kSums][32];                    // merge of the warps; combine scratch
+  float sums[kWarps][kSums][32];                    // merge of the warps
   float stat[kWarps][8][4];                         // m, l, m2 per warp and head
-  float fin[8][4];                                  // per head: M, M2, 1 / l, output factor
-  float fac[kMaxParts][8];                          // combine: a part's factor per head
-  int last[2];
 };
 
 struct Args {
@@ -75,7 +74,7 @@ struct Args {
   float* part;              // [2 CTAs][G][kPart]
   float* stats;             // [B * Hq][2]: M, 1 / l (nullptr: not wanted)
   float* scores;            // [B * Hq][score_stride] (nullptr: not wanted)
-  uint32_t* count;          // [units] parts done
+  int4* cuts;               // [CTAs]: the unit that ends behind this CTA: unit (2 words), parts
   uint32_t* err;
   int64_t score_stride;
   float scale_log2;
@@ -176,6 +175,7 @@ struct Tile {
 struct Rows {
   int row[2];
   uint32_t mask;
+  float ks, vs;         // !kUni: the scales of key i in lane i
 };
 
 __device__ __forceinline__ Tile no_tile() { return Tile{0, 0, 0, 0, -1, {0, 0}}; }
@@ -213,6 +213,7 @@ template <bool kUni>
 __device__ __forceinline__ Rows tile_rows(const Args& a, const Tile& t) {
   Rows r;
   r.row[0] = r.row[1] = -1;
+  r.ks = r.vs = 0.0f;
   r.mask = t.n >= 32 ? 0xffffffffu : (1u << t.n) - 1u;
   if constexpr (kUni) {
     if (a.c.table == nullptr) {
@@ -242,6 +243,8 @@ __device__ __forceinline__ Rows tile_rows(const Args& a, const Tile& t) {
                    (t.pos & ((1 << a.c.page_shift) - 1));
     }
     r.mask = __ballot_sync(0xffffffffu, r.row[0] >= 0);
+    r.ks = r.row[0] >= 0 ? __ldg(a.c.ks + (r.row[0] >> a.c.bshift)) : 0.0f;
+    r.vs = r.row[0] >= 0 ? __ldg(a.c.vs + (r.row[0] >> a.c.bshift)) : 0.0f;
   }
   return r;
 }
@@ -297,116 +300,140 @@ __device__ __forceinline__ float query_fragments(const QueryRow<T>& qr, float sc
   return scale_log2 * pow2i(e - 14);
 }
 
-// The even cut of T steps over C CTAs: the first T % C take one step more.
+// The even cut of a line over C CTAs, in grains (places, or whole units): the first CTAs take one
+// grain more where it does not come out even.
 struct Cut {
-  int q, r;
-  __device__ __forceinline__ int start(int c) const { return c * q + min(c, r); }
-  __device__ __forceinline__ int owner(int s) const {
+  int q, r, grain;
+  __device__ __forceinline__ int start(int c) const { return (c * q + min(c, r)) * grain; }
+  __device__ __forceinline__ int owner(int place) const {
+    const int s = grain == 1 ? place : place / grain;
     const int wide = r * (q + 1);
     return s < wide ? s / (q + 1) : r + (s - wide) / q;
   }
 };
 
-// Merges a unit's parts (in CTA order) into its output: the references and sums of every
-// head first (a warp per head), which gives each part's factor, then the sums over the parts,
-// threads = (part group, head, 4 dimensions) with kBatch loads under way each.
-template <int NT>
-__device__ __forceinline__ void combine_parts(const Args& a, Smem<NT>& sm, const Cut& cut,
-                                              int64_t unit, int u0, int c0, int parts) {
-  constexpr int kBatch = 16;
+// Whole units per CTA (equal units only) where that keeps 3 in 4 CTAs busy, since a unit in one piece
+// needs no second merge: 256 lists of 1024 positions on 296 CTAs take WHOLE_US us, cut evenly CUT_US.
+// 0: cut evenly.
+__host__ __device__ inline int whole_units(int units, int steps_per_unit, int grid) {
+  const int each = (units + grid - 1) / grid;
+  const bool few = int64_t(units) * steps_per_unit <= grid;
+  return !few && int64_t(units) * 4 >= int64_t(each) * grid * 3 ? each : 0;
+}
+
+// Merges the parts (in CTA order) of the units that were cut: block (c, h) takes head h of the unit
+// whose first part CTA c holds, if there is one.  Thread p finds part p's factor; then warp w sums
+// parts w, w + 8, ..., 4 dimensions per lane.
+constexpr int kCombineThreads = 256;
+
+__global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(
+    const int4* __restrict__ cuts, const float* __restrict__ part, int G, float* __restrict__ stats,
+    float* __restrict__ out) {
+  constexpr int kBatch = 10, kW = kCombineThreads / 32;
+  __shared__ float fac[kMaxParts];
+  __shared__ float red[3][kW];
+  __shared__ float4 sums[kW][32];
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x, h = blockIdx.y;
+  const int4 cut = cuts[c];
+  const int parts = cut.z;
+  if (parts < 2) return;
+  const int64_t unit = (int64_t(uint32_t(cut.y)) << 32) | uint32_t(cut.x);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int first = 2 * c0 + (cut.start(c0) < u0 ? 1 : 0);   // slot of part 0; then 2 (c0 + p)
-  const auto at = [&](int p, int h) {
-    return a.part + (int64_t(p == 0 ? first : 2 * (c0 + p)) * a.G + h) * kPart;
+  // a CTA's slot 1 holds the part of a unit that begins there, slot 0 that of one that goes on
+  const auto at = [&](int p) {
+    return reinterpret_cast<const float4*>(
+        part + (int64_t(2 * (c + p) + (p == 0 ? 1 : 0)) * G + h) * kPart);
   };
-  const int cols = a.G * (kD / 4);
-  const int groups = kThr / cols;
-  const int gr = tid / cols, ci = tid % cols;
-  const int hh = ci / (kD / 4), d4 = ci % (kD / 4);
   float4 y[kBatch];
   const auto load = [&](int p0) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int p = p0 + u * groups;
+      const int p = p0 + u * kW;
       y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (gr < groups && p < parts) y[u] = __ldcg(reinterpret_cast<const float4*>(at(p, hh) + 4) + d4);
+      if (p < parts) y[u] = __ldcg(at(p) + 1 + lane);
     }
   };
-  load(gr);   // under way while the factors are found
-  if (warp < a.G) {
-    float hM = -INFINITY, hM2 = -INFINITY;
-    float4 o[kMaxParts / 32];
+  load(warp);   // under way while the factors are found
+  float M = -INFINITY, M2 = -INFINITY;
+  float4 st[(kMaxParts + kCombineThreads - 1) / kCombineThreads];
 #pragma unroll
-    for (int i = 0; i < kMaxParts / 32; ++i) {
-      const int p = lane + 32 * i;
-      o[i] = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
-      if (p < parts) o[i] = __ldcg(reinterpret_cast<const float4*>(at(p, warp)));
-    }
-#pragma unroll
-    for (int i = 0; i < kMaxParts / 32; ++i) {
-      hM = fmaxf(hM, o[i].x);
-      hM2 = fmaxf(hM2, o[i].z);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      hM = fmaxf(hM, __shfl_xor_sync(0xffffffffu, hM, o));
-      hM2 = fmaxf(hM2, __shfl_xor_sync(0xffffffffu, hM2, o));
-    }
-    float hl = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kMaxParts / 32; ++i) {
-      hl += o[i].y * ref_change(o[i].x, hM);
-      if (lane + 32 * i < parts) sm.fac[lane + 32 * i][warp] = ref_change(o[i].z, hM2);
-    }
-    hl = warp_sum(hl);
-    if (lane == 0) {
-      const bool some = hl > 0.0f || !(hl == hl);
-      sm.fin[warp][3] = some ? ex2(hM2 - hM - kWBias) / hl : 0.0f;
-      if (a.stats != nullptr) {
-        float* const o = a.stats + (unit * a.G + warp) * 2;
-        o[0] = some ? hM : 0.0f;
-        o[1] = some ? 1.0f / hl : 0.0f;
-      }
-    }
+  for (int i = 0; i < int(sizeof(st) / sizeof(st[0])); ++i) {
+    const int p = tid + i * kCombineThreads;
+    st[i] = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+    if (p < parts) st[i] = __ldcg(at(p));
+    M = fmaxf(M, st[i].x);
+    M2 = fmaxf(M2, st[i].z);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    M2 = fmaxf(M2, __shfl_xor_sync(0xffffffffu, M2, o));
+  }
+  if (lane == 0) {
+    red[0][warp] = M;
+    red[1][warp] = M2;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kW; ++w) {
+    M = fmaxf(M, red[0][w]);
+    M2 = fmaxf(M2, red[1][w]);
+  }
+  float l = 0.0f;
+#pragma unroll
+  for (int i = 0; i < int(sizeof(st) / sizeof(st[0])); ++i) {
+    const int p = tid + i * kCombineThreads;
+    l += st[i].y * ref_change(st[i].x, M);
+    if (p < parts) fac[p] = ref_change(st[i].z, M2);
+  }
+  l = warp_sum(l);
+  if (lane == 0) red[2][warp] = l;
   __syncthreads();
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (gr < groups) {
-    for (int p0 = gr; p0 < parts; p0 += kBatch * groups) {
+  for (int p0 = warp; p0 < parts; p0 += kBatch * kW) {
+    if (p0 != warp) load(p0);
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int p = p0 + u * groups;
-        if (p < parts) {
-          const float f = sm.fac[p][hh];
-          t.x = fmaf(y[u].x, f, t.x);
-          t.y = fmaf(y[u].y, f, t.y);
-          t.z = fmaf(y[u].z, f, t.z);
-          t.w = fmaf(y[u].w, f, t.w);
-        }
+    for (int u = 0; u < kBatch; ++u) {
+      const int p = p0 + u * kW;
+      if (p < parts) {
+        const float f = fac[p];
+        t.x = fmaf(y[u].x, f, t.x);
+        t.y = fmaf(y[u].y, f, t.y);
+        t.z = fmaf(y[u].z, f, t.z);
+        t.w = fmaf(y[u].w, f, t.w);
       }
-      if (p0 + kBatch * groups < parts) load(p0 + kBatch * groups);
     }
   }
-  float4* const scratch = reinterpret_cast<float4*>(&sm.sums[0][0][0]);
-  scratch[tid] = t;
+  sums[warp][lane] = t;
   __syncthreads();
-  if (gr == 0) {
-    for (int g = 1; g < groups; ++g) {
-      const float4 x = scratch[g * cols + ci];
-      t.x += x.x;
-      t.y += x.y;
-      t.z += x.z;
-      t.w += x.w;
-    }
-    const float f = sm.fin[hh][3];
-    reinterpret_cast<float4*>(a.out + (unit * a.G + hh) * kD)[d4] =
-        make_float4(t.x * f, t.y * f, t.z * f, t.w * f);
+  if (warp != 0) return;
+  l = red[2][0];
+  t = sums[0][lane];
+#pragma unroll
+  for (int w = 1; w < kW; ++w) {
+    const float4 x = sums[w][lane];
+    l += red[2][w];
+    t.x += x.x;
+    t.y += x.y;
+    t.z += x.z;
+    t.w += x.w;
+  }
+  const bool some = l > 0.0f || !(l == l);
+  const float f = some ? ex2(M2 - M - kWBias) / l : 0.0f;
+  reinterpret_cast<float4*>(out + (unit * G + h) * kD)[lane] =
+      make_float4(t.x * f, t.y * f, t.z * f, t.w * f);
+  if (stats != nullptr && lane == 0) {
+    float* const o = stats + (unit * G + h) * 2;
+    o[0] = some ? M : 0.0f;
+    o[1] = some ? 1.0f / l : 0.0f;
   }
 }
 
 // FMT: byte format; NT: value products per 16 keys (1: G <= 4, 2: G <= 8).
 template <typename T, int FMT, int NT, bool kUni>
-__global__ void __launch_bounds__(kThr, 1) kv8_attention_kernel(const Args a) {
+__global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const Args a) {
   constexpr bool kLo = sizeof(T) == 4;   // fp32 queries take two fp16 parts
   using S = Smem<NT>;
   __shared__ __align__(16) S sm;
@@ -415,53 +442,74 @@ __global__ void __launch_bounds__(kThr, 1) kv8_attention_kernel(const Args a) {
   pdl_wait();
   pdl_trigger();
 
-  // ---- this CTA's steps [s0, s1) of the line of all units' steps
-  int s0, s1, C;
+  // ---- this CTA's part [x0, x1) of the line: per unit `cost` places that stand for its start and
+  // merge, then its steps
+  int x0, x1, cost;
   Cut cut;
   Place pf;
-  const auto cut_line = [&](int steps) {
-    C = min(int(gridDim.x), steps);
-    cut.q = C > 0 ? steps / C : 0;
-    cut.r = steps - cut.q * C;
+  const auto cut_over = [&](int grains, int ctas) {
+    const int C = min(ctas, grains);
+    cut.q = C > 0 ? grains / C : 0;
+    cut.r = grains - cut.q * C;
     const int cta = min(int(blockIdx.x), C);
-    s0 = cut.start(cta);
-    s1 = cut.start(min(cta + 1, C));
+    x0 = cut.start(cta);
+    x1 = cut.start(min(cta + 1, C));
   };
+  const int grid = int(gridDim.x);
+  int v = 0;   // place of the current step
+  // the first step at or after place x0 of a sequence of `len` keys whose first unit is at `base`
+  const auto begin = [&](int b, int len, int base) {
+    pf.b = b;
+    pf.len = len;
+    pf.ns = steps_of(len);
+    const int r = x0 - base, per = pf.ns + cost;
+    pf.j = r / per;
+    pf.ls = max(r - pf.j * per - cost, 0);
+    v = base + pf.j * per + cost + pf.ls;
+  };
+  cut.grain = 1;
   if (a.idx != nullptr || a.seq_lens == nullptr) {
-    pf.len = unit_len(a, 0, false);
-    pf.ns = steps_of(pf.len);
-    cut_line(a.c.B * a.U * pf.ns);
-    const int u = s0 / pf.ns;
-    pf.ls = s0 - u * pf.ns;
-    pf.b = u / a.U;
-    pf.j = u - pf.b * a.U;
+    const int len = unit_len(a, 0, false), ns = steps_of(len), units = a.c.B * a.U;
+    // fewer steps than CTAs: one each, and no places for starts and merges
+    cost = units * ns > grid ? kUnitCost : 0;
+    const int each = whole_units(units, ns, grid);
+    if (each > 0) {
+      cut.grain = ns + cost;
+      cut_over(units, (units + each - 1) / each);
+    } else {
+      cut_over(units * (ns + cost), cost > 0 ? grid : units * ns);
+    }
+    const int per = a.U * (ns + cost), b = x0 / per;
+    begin(b, len, b * per);
   } else {
     // every warp for itself: lane l sums sequences l, l + 32, ..., then prefix sums over 32
-    // sequences at a time find the one that holds step s0
-    int mine = 0;
-    for (int b = lane; b < a.c.B; b += 32)
-      mine += steps_of(unit_len(a, b, blockIdx.x == 0 && warp == 0));
-    cut_line(__reduce_add_sync(0xffffffffu, mine) * a.U);
+    // sequences at a time find the one that holds place x0
+    int mine = 0, some = 0;
+    for (int b = lane; b < a.c.B; b += 32) {
+      const int n = steps_of(unit_len(a, b, blockIdx.x == 0 && warp == 0));
+      mine += n;
+      some += n > 0;
+    }
+    const int steps = __reduce_add_sync(0xffffffffu, mine) * a.U;
+    cost = steps > grid ? kUnitCost : 0;
+    cut_over(steps + cost * __reduce_add_sync(0xffffffffu, some) * a.U, cost > 0 ? grid : steps);
     int before = 0;
-    for (int b0 = 0; s0 < s1; b0 += 32) {
+    for (int b0 = 0; x0 < x1; b0 += 32) {
       const int b = b0 + lane;
       const int full = b < a.c.B ? unit_len(a, b, false) : 0;
-      const int n = steps_of(full) * a.U;
+      const int ns = steps_of(full);
+      const int n = ns > 0 ? (ns + cost) * a.U : 0;
       int inc = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += y;
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, before + inc > s0);
+      const unsigned hit = __ballot_sync(0xffffffffu, before + inc > x0);
       if (hit) {
         const int at = __ffs(hit) - 1;
-        pf.b = b0 + at;
-        pf.len = __shfl_sync(0xffffffffu, full, at);
-        pf.ns = steps_of(pf.len);
-        const int r = s0 - (before + __shfl_sync(0xffffffffu, inc - n, at));
-        pf.j = r / pf.ns;
-        pf.ls = r - pf.j * pf.ns;
+        begin(b0 + at, __shfl_sync(0xffffffffu, full, at),
+              before + __shfl_sync(0xffffffffu, inc - n, at));
         break;
       }
       before += __shfl_sync(0xffffffffu, inc, 31);
@@ -476,7 +524,10 @@ __global__ void __launch_bounds__(kThr, 1) kv8_attention_kernel(const Args a) {
           a.stats[int64_t(b) * a.U * a.G * 2 + i] = 0.0f;
     }
   }
-  if (s0 >= s1) return;
+  if (x0 >= x1 || v >= x1) {
+    if (tid == 0) a.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+    return;
+  }
   const int head = NT == 1 ? (gid & 3) : gid;       // this lane's head row
   const bool head_ok = head < a.G;
   // the queries first: they are needed as soon as the first keys are
@@ -510,10 +561,9 @@ __global__ void __launch_bounds__(kThr, 1) kv8_attention_kernel(const Args a) {
           kreg[u][2 * tau + 1] = load_row16(p + 64, kFull || row >= 0);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = __shfl_sync(0xffffffffu, r.row[0], 16 * u + 8 * (i >> 1) + 2 * q + (i & 1));
-          ksc[u][kUni ? 0 : i] = kFull || row >= 0 ? __ldg(a.c.ks + (row >> a.c.bshift)) : 0.0f;
-        }
+        for (int i = 0; i < 4; ++i)
+          ksc[u][kUni ? 0 : i] =
+              __shfl_sync(0xffffffffu, r.ks, 16 * u + 8 * (i >> 1) + 2 * q + (i & 1));
       }
     }
   };
@@ -535,7 +585,8 @@ __global__ void __launch_bounds__(kThr, 1) kv8_attention_kernel(const Args a) {
         for (int i = 0; i < 4; ++i) {
           const int row = __shfl_sync(0xffffffffu, r.row[0], 16 * u + 8 * (i >> 1) + 2 * q + (i & 1));
           vreg[u][i] = load_row16(a.c.v + int64_t(row) * kD + 16 * gid, kFull || row >= 0);
-          vsc[u][kUni ? 0 : i] = kFull || row >= 0 ? __ldg(a.c.vs + (row >> a.c.bshift)) : 0.0f;
+          vsc[u][kUni ? 0 : i] =
+              __shfl_sync(0xffffffffu, r.vs, 16 * u + 8 * (i >> 1) + 2 * q + (i & 1));
         }
       }
     }
@@ -560,9 +611,10 @@ __global__ void __launch_bounds__(kThr, 1) kv8_attention_kernel(const Args a) {
   // Tiles under way: r0 in registers (or coming), r1 the next one, tb with its pages and ta with
   // its positions coming.
   Place cur = pf;
-  int placed = s0;
+  int placed = v;   // place of pf's step
   const auto next_tile = [&]() {
-    if (++placed >= s1) return no_tile();
+    placed += pf.ls + 1 < pf.ns ? 1 : 1 + cost;
+    if (placed >= x1) return no_tile();
     next_place(a, pf);
     return tile_positions<kUni>(a, pf, warp, lane);
   };
@@ -595,10 +647,8 @@ __global__ void __launch_bounds__(kThr, 1) kv8_attention_kernel(const Args a) {
   float m = -INFINITY, m2 = -INFINITY, l = 0.0f;
   float acc[8][4];
   bool fresh = true;
-  int64_t open_unit[2] = {0, 0};   // units this CTA holds a part of
-  int open_u0[2] = {0, 0}, open_parts[2] = {0, 0};
-  uint32_t before[2] = {0u, 0u};
-  for (int s = s0; s < s1; ++s) {
+  int4 cut_here = make_int4(0, 0, 0, 0);   // the unit that begins here and ends in a later CTA
+  for (;;) {
     const int64_t unit = int64_t(cur.b) * a.U + cur.j;
     if (fresh) {
       factor = query_fragments<T, kLo>(qrow, a.scale_log2, qh, ql);
@@ -775,12 +825,15 @@ __global__ void __launch_bounds__(kThr, 1) kv8_attention_kernel(const Args a) {
     r0 = r1;
     r1 = r2;
 
-    const int u0 = s - cur.ls;                  // the unit's first step
+    const int u0 = v - cur.ls;                  // the place of the unit's first step
     const int unit_end = u0 + cur.ns;
-    if (s + 1 < s1 && s + 1 < unit_end) {
+    if (v + 1 < x1 && v + 1 < unit_end) {
       ++cur.ls;
+      ++v;
     } else {
-      if (s + 1 < s1) {
+      const int next_v = unit_end + cost;
+      const bool more = next_v < x1;
+      if (more) {
         // the next unit's queries come while this one's states are merged
         next_place(a, cur);
         qrow.load(a.q, (int64_t(cur.b) * a.U + cur.j) * a.G + head, head_ok, q);
@@ -793,128 +846,76 @@ __global__ void __launch_bounds__(kThr, 1) kv8_attention_kernel(const Args a) {
         sm.stat[warp][head][1] = l;
         sm.stat[warp][head][2] = m2;
       }
-      __syncthreads();
-      float M2 = -INFINITY;
+      // High and low parts together.  NT = 1: lanes q and q ^ 2 hold the two parts of two
+      // heads; each keeps half of the dimensions (value 4 t + i: tile t + 4 (q / 2)).
+      // NT = 2: value 4 t + i: tile t.
+      if constexpr (NT == 1) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M2 = fmaxf(M2, sm.stat[w][head][2]);
-      {
-        const float r = ref_change(m2, M2);
-        const float f0 = __shfl_sync(0xffffffffu, r, 8 * q);
-        const float f1 = __shfl_sync(0xffffffffu, r, 8 * q + 4);
-        // High and low parts together, at the merged reference.  NT = 1: lanes q and q ^ 2
-        // hold the two parts of two heads; each keeps half of the dimensions (value 4 t + i:
-        // tile t + 4 (q / 2)).  NT = 2: value 4 t + i: tile t.
-        if constexpr (NT == 1) {
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
+          for (int i = 0; i < 4; ++i) {
+            const float keep = (q & 2) ? acc[t + 4][i] : acc[t][i];
+            const float give = (q & 2) ? acc[t][i] : acc[t + 4][i];
+            sm.sums[warp][4 * t + i][lane] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+          }
+      } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float keep = (q & 2) ? acc[t + 4][i] : acc[t][i];
-              const float give = (q & 2) ? acc[t][i] : acc[t + 4][i];
-              sm.sums[warp][4 * t + i][lane] =
-                  (keep + __shfl_xor_sync(0xffffffffu, give, 2)) * ((i & 1) ? f1 : f0);
-            }
-        } else {
+        for (int t = 0; t < 8; ++t)
 #pragma unroll
-          for (int t = 0; t < 8; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              sm.sums[warp][4 * t + i][lane] =
-                  acc[t][i] * ((i & 1) ? f1 : f0);
-        }
-      }
-      if (warp < a.G) {   // head `warp`: lane w takes warp w's state
-        const float wm = lane < kWarps ? sm.stat[lane % kWarps][warp][0] : -INFINITY;
-        const float wl = lane < kWarps ? sm.stat[lane % kWarps][warp][1] : 0.0f;
-        const float wm2 = lane < kWarps ? sm.stat[lane % kWarps][warp][2] : -INFINITY;
-        float hM = wm, hM2 = wm2;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          hM = fmaxf(hM, __shfl_xor_sync(0xffffffffu, hM, o));
-          hM2 = fmaxf(hM2, __shfl_xor_sync(0xffffffffu, hM2, o));
-        }
-        const float hl = warp_sum(wl * ref_change(wm, hM));
-        if (lane == 0) {
-          const bool some = hl > 0.0f || !(hl == hl);   // an empty list: zeros
-          sm.fin[warp][0] = hM;
-          sm.fin[warp][1] = hM2;
-          sm.fin[warp][2] = hl;
-          sm.fin[warp][3] = some ? ex2(hM2 - hM - kWBias) / hl : 0.0f;
-        }
+          for (int i = 0; i < 4; ++i) sm.sums[warp][4 * t + i][lane] = acc[t][i];
       }
       __syncthreads();
       // ---- the unit's parts: CTAs c0 .. c0 + parts - 1 hold steps of it
       const int c0 = cut.owner(u0);
       const int parts = cut.owner(unit_end - 1) - c0 + 1;
-      // slot 0: the CTA's first unit, slot 1: its last when that is another one
-      float* const slot = a.part + int64_t(2 * blockIdx.x + (u0 > s0 ? 1 : 0)) * a.G * kPart;
+      // slot 0: the part of a unit that began before, slot 1: of one that begins here
+      const int which = u0 >= x0 ? 1 : 0;
+      float* const slot = a.part + int64_t(2 * blockIdx.x + which) * a.G * kPart;
       // value v of lane (gid, q) of the fragments: head 2 q (NT = 1: 2 (q % 2)) + v % 2,
       // dimension 16 gid (+ 8 (q / 2)) + v / 2; thread (head, 4 dimensions) sums the warps
       for (int i = tid; i < a.G * (kD / 4); i += kThr) {
         const int hh = i / (kD / 4), d = 4 * (i % (kD / 4));
+        float hM = -INFINITY, hM2 = -INFINITY, hl = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          hM = fmaxf(hM, sm.stat[w][hh][0]);
+          hM2 = fmaxf(hM2, sm.stat[w][hh][2]);
+        }
         const int ln = 4 * (d >> 4) + (NT == 1 ? (hh >> 1) + 2 * ((d >> 3) & 1) : hh >> 1);
         const int v0 = 2 * (NT == 1 ? d & 7 : d & 15) + (hh & 1);
         float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
+        for (int w = 0; w < kWarps; ++w) {
+          hl += sm.stat[w][hh][1] * ref_change(sm.stat[w][hh][0], hM);
+          const float f = ref_change(sm.stat[w][hh][2], hM2);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) t[e] += sm.sums[w][v0 + 2 * e][ln];
+          for (int e = 0; e < 4; ++e) t[e] = fmaf(sm.sums[w][v0 + 2 * e][ln], f, t[e]);
+        }
         if (parts == 1) {
-          const float f = sm.fin[hh][3];
+          const bool some = hl > 0.0f || !(hl == hl);   // an empty list: zeros
+          const float f = some ? ex2(hM2 - hM - kWBias) / hl : 0.0f;
           *reinterpret_cast<float4*>(a.out + (unit * a.G + hh) * kD + d) =
               make_float4(t[0] * f, t[1] * f, t[2] * f, t[3] * f);
-        } else {
-          *reinterpret_cast<float4*>(slot + hh * kPart + 4 + d) =
-              make_float4(t[0], t[1], t[2], t[3]);
-        }
-      }
-      if (tid < a.G) {
-        if (parts == 1) {
-          if (a.stats != nullptr) {
-            float* const o = a.stats + (unit * a.G + tid) * 2;
-            const float hl = sm.fin[tid][2];
-            const bool some = hl > 0.0f || !(hl == hl);
-            o[0] = some ? sm.fin[tid][0] : 0.0f;
+          if (d == 0 && a.stats != nullptr) {
+            float* const o = a.stats + (unit * a.G + hh) * 2;
+            o[0] = some ? hM : 0.0f;
             o[1] = some ? 1.0f / hl : 0.0f;
           }
         } else {
-          float* const o = slot + tid * kPart;
-          o[0] = sm.fin[tid][0];
-          o[1] = sm.fin[tid][2];
-          o[2] = sm.fin[tid][1];
+          *reinterpret_cast<float4*>(slot + hh * kPart + 4 + d) =
+              make_float4(t[0], t[1], t[2], t[3]);
+          if (d == 0)
+            *reinterpret_cast<float4*>(slot + hh * kPart) = make_float4(hM, hl, hM2, 0.0f);
         }
       }
-      __syncthreads();   // the parts are written; sums, stat and fin are free again
-      if (parts > 1) {
-        // a CTA has at most two parts: its first unit's and its last unit's.  Whether a unit is
-        // complete is looked at when the CTA is done, so nothing waits for the count here.
-        const int which = u0 > s0 ? 1 : 0;
-        open_unit[which] = unit;
-        open_u0[which] = u0;
-        open_parts[which] = parts;
-        if (tid == 0) {
-          __threadfence();
-          before[which] = atomicAdd(a.count + unit, 1u);
-        }
-      }
+      __syncthreads();   // the part is written; sums and stat are free again
+      if (parts > 1 && which == 1) cut_here = make_int4(int(unit), int(unit >> 32), parts, 0);
       fresh = true;
+      if (!more) break;
+      v = next_v;
     }
   }
-  if (open_parts[0] + open_parts[1] == 0) return;
-  if (tid == 0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      sm.last[i] = open_parts[i] > 0 && before[i] + 1u == uint32_t(open_parts[i]);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (!sm.last[i]) continue;
-    __threadfence();
-    combine_parts<NT>(a, sm, cut, open_unit[i], open_u0[i], cut.owner(open_u0[i]), open_parts[i]);
-    if (tid == 0) a.count[open_unit[i]] = 0u;
-    __syncthreads();
-  }
+  if (tid == 0) a.cuts[blockIdx.x] = cut_here;
 }
 
 // ------------------------------------------------------------- attention weights
@@ -1006,12 +1007,18 @@ __global__ void __launch_bounds__(512) kv8_sparse_weights_kernel(
 // CTAs of the attention kernel: the co-resident ones, no more than there can be steps.
 int attention_ctas(int64_t units, int64_t len, int sms) {
   const int64_t steps = units * ((len + kStep - 1) / kStep);
-  const int64_t room = sms < kMaxParts ? sms : kMaxParts;
+  const int64_t room = sms * kCtasPerSm < kMaxParts ? sms * kCtasPerSm : kMaxParts;
   return int(steps < room ? steps : room);
 }
 
+// Whether units may be cut between CTAs (then the combine kernel follows).
+bool cuts_units(int64_t units, int64_t len, bool equal, int ctas) {
+  const int64_t per = (len + kStep - 1) / kStep;
+  return per > 1 && !(equal && whole_units(int(units), int(per), ctas));
+}
+
 struct Room {
-  size_t count, part, stats, scores, total;
+  size_t cuts, part, stats, scores, total;
   int64_t stride;
 };
 Room workspace_room(int B, int Hq, int Hkv, int64_t Lmax, int k, bool shared, bool weights) {
@@ -1019,9 +1026,9 @@ Room workspace_room(int B, int Hq, int Hkv, int64_t Lmax, int k, bool shared, bo
   const int64_t U = sparse && !shared ? Hq : Hkv;
   const int G = int(Hq / U);
   Room r;
-  r.count = 256;
-  r.part = r.count + align_up(size_t(B) * U * 4, 256);
   const int ctas = attention_ctas(B * U, sparse ? k : Lmax, device_sms());
+  r.cuts = 256;
+  r.part = r.cuts + align_up(size_t(ctas) * sizeof(int4), 256);
   r.stats = r.part + align_up(size_t(ctas) * 2 * G * kPart * 4, 256);
   r.scores = r.stats + (weights ? align_up(size_t(B) * Hq * 8, 256) : 0);
   // rows padded to whole warp tiles: the kernel stores scores tile by tile
@@ -1072,7 +1079,7 @@ cudaError_t launch_kv8_attention(const Kv8& c, int fmt, const void* q, adamas_dt
   a.idx = idx;
   a.out = out;
   a.err = reinterpret_cast<uint32_t*>(base + decode_workspace_error_offset());
-  a.count = reinterpret_cast<uint32_t*>(base + r.count);
+  a.cuts = reinterpret_cast<int4*>(base + r.cuts);
   a.part = reinterpret_cast<float*>(base + r.part);
   a.stats = weights ? reinterpret_cast<float*>(base + r.stats) : nullptr;
   a.scores = weights ? reinterpret_cast<float*>(base + r.scores) : nullptr;
@@ -1091,7 +1098,7 @@ cudaError_t launch_kv8_attention(const Kv8& c, int fmt, const void* q, adamas_dt
   else
     e = fmt == kFmtE4m3 ? run_attention_g<float, kFmtE4m3>(a, ctas, uni, stream)
                         : run_attention_g<float, kFmtInt8>(a, ctas, uni, stream);
-  if (e != cudaSuccess || !weights) return e;
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1099,6 +1106,15 @@ cudaError_t launch_kv8_attention(const Kv8& c, int fmt, const void* q, adamas_dt
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (cuts_units(int64_t(c.B) * a.U, idx ? k : c.Lmax, idx != nullptr || seq_lens == nullptr, ctas)) {
+    cfg.gridDim = dim3(unsigned(ctas), unsigned(a.G));
+    cfg.blockDim = dim3(kCombineThreads);
+    e = cudaLaunchKernelEx(&cfg, kv8_combine_kernel, static_cast<const int4*>(a.cuts),
+                           static_cast<const float*>(a.part), a.G, a.stats, out);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(1);
+  }
+  if (!weights) return cudaSuccess;
   const int64_t units = int64_t(c.B) * c.Hkv;
   const int G = Hq / c.Hkv;
   if (idx == nullptr) {
