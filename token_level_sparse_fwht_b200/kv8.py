@@ -131,7 +131,13 @@ def _where(device, stream):
 def _owner(device, stream):
     """Tensors made inside belong to the call's device and stream."""
     index, handle = _where(device, stream)
-    with torch.cuda.device(index), torch.cuda.stream(torch.cuda.ExternalStream(handle, index)):
+    with contextlib.ExitStack() as stack:
+        if torch.cuda.current_device() != index:
+            stack.enter_context(torch.cuda.device(index))
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(handle, index)
+            stack.enter_context(torch.cuda.stream(stream))
         yield
 
 
