@@ -719,3 +719,134 @@ def test_same_call_twice_is_bitwise_the_same():
     fine(ws)
     for o, w in got[1:]:
         assert torch.equal(o, got[0][0]) and torch.equal(w, got[0][1])
+
+
+def test_rows_beyond_four_gigabytes():
+    """Row offsets past 2^32 bytes: append, read, sparse and (over pages) dense attention, eviction's move
+    at the far end of a cache of 40 million rows."""
+    rows, L = 40_000_000, 20_000_000
+    free, _ = torch.cuda.mem_get_info()
+    if free < 2.5 * rows * 128 * 2:
+        pytest.skip("needs 26 GB free")
+    byte = torch.zeros((2, rows * 128), dtype=torch.uint8, device="cuda")
+    scale = torch.zeros((2, rows // 64), device="cuda")
+    view = lambda t, *s: t.view(torch.float8_e4m3fn).view(*s) if t.dtype == torch.uint8 else t.view(*s)  # noqa: E731
+    flat = ad.KV8Cache(view(byte[0], 2, 1, L, 128), view(byte[1], 2, 1, L, 128), scale[0].view(2, 1, -1),
+                       scale[1].view(2, 1, -1), 64)
+    ws = ad.kv8_sparse_attention_workspace(2, 4, 1, 64)
+    x = torch.randn((2, 2, 1, 128, 128), generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    start = L - 128
+    ad.kv8_append(flat, x[0], x[1], start, ws)
+    k, v = ad.kv8_read(flat, start, 128, ws, torch.float32)
+    q = _q(2, 4, torch.bfloat16, 5)
+    idx = (start + torch.arange(64, device="cuda", dtype=torch.int32) * 2).expand(2, 4, 64).contiguous()
+    out = ad.kv8_sparse_attention(q, flat, idx, ws)
+    fine(ws)
+    K, V = (t.double().cpu().numpy() for t in (k, v))
+    C = scale[1].view(2, 1, -1)[:, :, start // 64:].double().cpu().numpy().repeat(64, 2)
+    want, tol, _, _ = attention_oracle(q.double().cpu().numpy(), (K, V, C), lambda b, h: np.arange(64) * 2)
+    check(out, want, tol, "sparse")
+    for b in range(2):
+        st, sc = ref.append(np.zeros((128, 128)), np.zeros(2), x[0, b, 0].double().cpu().numpy(), 0, "e4m3", 64)
+        assert np.array_equal(K[b, 0], st * sc.repeat(64)[:, None])
+    # the same memory as pages of 64 rows: a sequence on the last two pages
+    pages = rows // 64
+    paged = ad.KV8Cache(view(byte[0], pages, 1, 64, 128), view(byte[1], pages, 1, 64, 128),
+                        scale[0].view(pages, 1, 1), scale[1].view(pages, 1, 1), 64,
+                        block_table=i32([[pages - 2, pages - 1]]))
+    dws = ad.kv8_attention_workspace(1, 4, 1, 128)
+    out = ad.kv8_attention(q[1:], paged, i32([100]), dws)
+    fine(dws)
+    want, tol, _, _ = attention_oracle(q[1:].double().cpu().numpy(), (K[1:], V[1:], C[1:]),
+                                       lambda b, h: np.arange(100))
+    check(out, want, tol, "paged")
+    # eviction in place moves the last page's rows down to the one before
+    w = torch.zeros((1, 1, 128), device="cuda")
+    w[..., 64:] = 1.0
+    keep, lens = ad.kv8_evict(paged, w, i32([128]), 64, dws)
+    fine(dws)
+    assert keep[0, 0].tolist() == list(range(64, 128)) and lens.tolist() == [64]
+    got, _ = ad.kv8_read(paged, 0, 64, dws, torch.float32)
+    assert np.array_equal(got[0, 0].double().cpu().numpy(), K[1, 0, 64:])
+
+
+def test_a_serving_step_in_one_graph():
+    """append, sparse attention with weights and eviction into a second cache, captured together and
+    replayed with new rows, queries and lengths: equal to eager calls."""
+    B, Hkv, Hq, L, kk = 2, 2, 4, 256, 20
+    base = Case(B, Hkv, L, "e4m3", block=16, seed=31)
+
+    def setup():
+        c = base.upload(ad)
+        d = Case(B, Hkv, 96, "e4m3", block=16, empty=True).upload(ad)
+        return dict(c=c, d=d, x=torch.zeros((2, B, Hkv, 1, D), dtype=torch.bfloat16, device="cuda"),
+                    q=_q(B, Hq, torch.bfloat16), lens=i32([0, 0]), idx=i32([[[0] * kk] * Hq] * B),
+                    w=torch.zeros((B, Hkv, L), device="cuda"), w2=torch.zeros((B, Hkv, 96), device="cuda"),
+                    out=torch.empty((B, Hq, D), device="cuda"), lens2=i32([0, 0]), now=i32([0, 0]),
+                    keep=torch.empty((B, Hkv, 90), dtype=torch.int32, device="cuda"),
+                    ws=ad.kv8_sparse_attention_workspace(B, Hq, Hkv, kk, weights=True))
+
+    def step(s):
+        ad.PreparedKV8Append(s["c"], s["x"][0], s["x"][1], s["lens"], s["ws"])()
+        torch.add(s["lens"], 1, out=s["now"])
+        ad.PreparedKV8SparseAttention(s["q"], s["c"], s["idx"], s["ws"], s["out"], weights=s["w"])()
+        ad.PreparedKV8Evict(s["c"], s["d"], s["w"], s["w2"], s["now"], s["lens2"], s["keep"], 90, 2, 8,
+                            s["ws"])()
+
+    a, b = setup(), setup()
+    step(a)
+    torch.cuda.synchronize()
+    a = setup()
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        step(a)
+    rng = np.random.default_rng(3)
+    for lens in ([100, 80], [200, 17], [255, 90]):
+        x = torch.from_numpy(rng.standard_normal((2, B, Hkv, 1, D))).to(torch.bfloat16)
+        idx = np.stack([np.stack([np.sort(rng.choice(n, min(n, kk), replace=False)) for _ in range(Hq)])
+                        if n >= kk else np.tile(np.r_[0:n, [-1] * (kk - n)], (Hq, 1)) for n in lens])
+        for s in (a, b):
+            s["x"].copy_(x)
+            s["q"].copy_(_q(B, Hq, torch.bfloat16, lens[0]))
+            s["lens"].copy_(i32(lens))
+            s["idx"].copy_(up(idx.astype(np.int32)))
+        graph.replay()
+        step(b)
+        torch.cuda.synchronize()
+        for n in ("out", "w", "w2", "lens2", "keep"):
+            assert torch.equal(a[n], b[n]), n
+        for n in ("c", "d"):
+            assert torch.equal(a[n].k.view(torch.uint8), b[n].k.view(torch.uint8))
+            assert torch.equal(a[n].v_scale, b[n].v_scale)
+    fine(a["ws"])
+    fine(b["ws"])
+
+
+def test_append_of_broadcast_rows():
+    """Stride 0: one row's values given to every head."""
+    c = Case(1, 4, 32, "int8", block=8, seed=2)
+    cache = c.upload(ad)
+    x = torch.randn((1, 1, 5, D), generator=torch.Generator().manual_seed(0)).cuda().expand(1, 4, 5, D)
+    ws = ad.kv8_workspace()
+    ad.kv8_append(cache, x, x, 9, ws)
+    fine(ws)
+    k, ks, _, _, _ = c.download(cache)
+    for h in range(4):
+        st, sc = ref.append(c.k[0, h], c.ks[0, h], x[0, 0].double().cpu().numpy(), 9, "int8", 8)
+        assert np.array_equal(k[0, h], st) and np.array_equal(ks[0, h], sc)
+
+
+def test_a_larger_workspace_serves_smaller_calls():
+    c = Case(1, 2, 300, "e4m3", block=16, seed=2)
+    cache, q = c.upload(ad), _q(1, 8, torch.bfloat16)
+    big = ad.kv8_attention_workspace(4, 32, 8, 4096, weights=True)
+    small = ad.kv8_attention_workspace(1, 8, 2, cache.Lmax)
+    for _ in range(2):
+        a = ad.kv8_attention(q, cache, i32([300]), big)
+        w = torch.zeros((1, 2, cache.Lmax), device="cuda")
+        b = ad.kv8_attention(q, cache, i32([300]), big, weights=w)
+        assert torch.equal(a, b) and torch.equal(a, ad.kv8_attention(q, cache, i32([300]), small))
+    with pytest.raises(ad.AdamasError):
+        ad.kv8_attention(q, cache, i32([300]), small, weights=w)
+    fine(big)

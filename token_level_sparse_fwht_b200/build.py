@@ -12,6 +12,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -47,18 +49,34 @@ def build(verbose: bool = False, force: bool = False) -> str:
     if not force and not needs_rebuild():
         return LIB
     tmp = LIB + ".tmp"
-    cmd = [nvcc(), *ARCH, *FLAGS, "-shared", "-I", INCLUDE, "-I", CSRC, *sources(), "-o", tmp]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd))
+    with tempfile.TemporaryDirectory() as objs:
+        # one compiler per source file, side by side
+        jobs = []
+        for src in sources():
+            obj = os.path.join(objs, os.path.basename(src)[:-3] + ".o")
+            cmd = [nvcc(), *ARCH, *FLAGS, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj]
+            if verbose:
+                cmd.insert(1, "-Xptxas=-v")
+                print(" ".join(cmd))
+            jobs.append((obj, cmd))
+        with ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:
+            for ok in pool.map(lambda job: _run(job[1], verbose), jobs):
+                if not ok:
+                    raise RuntimeError("nvcc failed building libadamas.so")
+        if not _run([nvcc(), *ARCH, "-cudart", "static", "-shared", *(o for o, _ in jobs), "-o", tmp],
+                    verbose):
+            raise RuntimeError("nvcc failed linking libadamas.so")
+    os.replace(tmp, LIB)
+    return LIB
+
+
+def _run(cmd, verbose: bool) -> bool:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("nvcc failed building libadamas.so")
-    if verbose:
+    elif verbose:
         sys.stdout.write(res.stdout + res.stderr)
-    os.replace(tmp, LIB)
-    return LIB
+    return res.returncode == 0
 
 
 if __name__ == "__main__":

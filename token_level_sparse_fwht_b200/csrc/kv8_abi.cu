@@ -34,7 +34,12 @@ namespace {
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 bool pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
-adamas_status from_cuda(cudaError_t e) { return e == cudaSuccess ? ADAMAS_OK : ADAMAS_ERR_CUDA; }
+// The launchers answer cudaErrorNotSupported for sizes that no grid holds.
+adamas_status from_cuda(cudaError_t e) {
+  return e == cudaSuccess             ? ADAMAS_OK
+         : e == cudaErrorNotSupported ? ADAMAS_ERR_UNSUPPORTED
+                                      : ADAMAS_ERR_CUDA;
+}
 bool good_dtype(adamas_dtype dt) { return dt == ADAMAS_F32 || dt == ADAMAS_BF16; }
 
 constexpr int64_t kMaxLen = int64_t(1) << 30;   // positions of a sequence (int32 arithmetic)

@@ -278,7 +278,7 @@ static cudaError_t append_t(const Kv8& c, int fmt, const void* kn, const void* v
   const int64_t per_seq = (n_new + 2 * int64_t(bs) - 2) / bs;
   const int64_t items = int64_t(c.B) * c.Hkv * 2 * per_seq;
   const int64_t grid = (items + teams - 1) / teams;
-  if (items + teams > INT32_MAX) return cudaErrorInvalidValue;
+  if (items + teams > INT32_MAX) return cudaErrorNotSupported;   // more blocks than a grid holds
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
   cfg.blockDim = dim3(unsigned(warps * 32));
@@ -395,7 +395,7 @@ static cudaError_t read_t(const Kv8& c, int fmt, const int32_t* starts, int64_t 
                           void* vo, uint32_t* err, cudaStream_t stream) {
   const int64_t tiles = (n + kReadRows - 1) / kReadRows;
   const int64_t grid = int64_t(c.B) * c.Hkv * tiles;
-  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  if (grid > INT32_MAX) return cudaErrorNotSupported;   // more blocks than a grid holds
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid), 2);
   cfg.blockDim = dim3(kReadThreads);

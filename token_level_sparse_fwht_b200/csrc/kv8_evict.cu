@@ -521,7 +521,7 @@ cudaError_t launch_evict_select(const float* w, int B, int Hkv, int64_t Lmax,
   while (cs < 8 && Lmax > int64_t(cs) * 4096 && units * cs * 2 <= 2 * device_sms()) cs *= 2;
   while (Lmax > int64_t(cs) * kMaxShare) cs *= 2;
   const int share = int((Lmax + cs - 1) / cs + 31) / 32 * 32;
-  if (units * cs > INT32_MAX) return cudaErrorInvalidValue;
+  if (units * cs > INT32_MAX) return cudaErrorNotSupported;   // more blocks than a grid holds
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cluster_config(cfg, attr, cs);
@@ -543,7 +543,7 @@ cudaError_t launch_kv8_compact(const Kv8& src, const Kv8& dst, int fmt, const in
   const int rows = move_per(in_place) * threads / 4;
   const int64_t cs = in_place ? move_cluster(n_keep, rows, units * parts)
                               : (int64_t(n_keep) + rows - 1) / rows;
-  if (units * parts * cs > INT32_MAX) return cudaErrorInvalidValue;
+  if (units * parts * cs > INT32_MAX) return cudaErrorNotSupported;   // more blocks than a grid holds
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cluster_config(cfg, attr, in_place ? int(cs) : 1);
@@ -566,7 +566,7 @@ cudaError_t launch_compact_rows(const Kv8& lay, const void* src, void* dst, int 
   while ((16 << pshift) < row_bytes) ++pshift;
   const int64_t units = int64_t(lay.B) * lay.Hkv;
   const int cs = move_cluster(n_keep, (kMoveThreads * 8) >> pshift, units);
-  if (units * cs > INT32_MAX) return cudaErrorInvalidValue;
+  if (units * cs > INT32_MAX) return cudaErrorNotSupported;   // more blocks than a grid holds
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   cluster_config(cfg, attr, cs);
