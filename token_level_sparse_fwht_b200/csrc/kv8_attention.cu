@@ -28,17 +28,21 @@
 //
 // Layout of the work.  A step is 128 keys of a unit: 32 per warp, 4 warps.  The steps of all
 // units form one line (with kUnitCost places more per unit, for what its start and its merge cost)
-// that is cut evenly over the CTAs; lengths are read on the device, so unequal sequences balance; a CTA's cut may hold the end of one unit, whole units and
-// the start of another.  Each lane loads the 16-byte pieces of K and V rows that its fragments
-// need straight into registers: a tile's K registers are refilled (with the next tile, of the next
-// unit if need be) as soon as its scores are formed, the V registers after its value product,
-// so 8 KB per warp stay under way through the rest of the work.  At a unit's end the warps'
-// states are merged; a unit cut between CTAs leaves its parts in the workspace, and a second kernel,
-// which is launched early and waits, merges them in CTA order.
+// that is cut evenly over the CTAs; lengths are read on the device, so unequal sequences balance;
+// a CTA's cut may hold the end of one unit, whole units and the start of another.  At a unit's end
+// the warps' states are merged; a unit cut between CTAs leaves its parts in the workspace, and a
+// second kernel, which is launched early and waits, merges them in CTA order.
 //
-// kUni: 16 rows of a tile follow one another and share one scale (contiguous caches and pages
-// of at least 16 rows, blocks of at least 16 positions); otherwise (given positions, small
-// pages or blocks) rows and scales are looked up key by key.
+// kUni: 16 rows of a tile follow one another and share one scale (contiguous caches and pages of
+// at least 16 rows, blocks of at least 16 positions).  Each lane loads the 16-byte pieces of K and
+// V rows that its fragments need straight into registers: a tile's K registers are refilled (with
+// the next tile, of the next unit if need be) as soon as its scores are formed, the V registers
+// after its value product, so 8 KB per warp stay under way through the rest of the work, and the
+// tile behind it has been asked into L2.
+// Otherwise (given positions, small pages or blocks) rows and scales are looked up key by key, three
+// tiles ahead, and the rows come by cp.async through a ring of three tiles per warp: a tile has a
+// whole tile's time more to arrive, and a row's address is formed once instead of by every lane
+// that holds a piece of it.
 #include <type_traits>
 
 #include "kv8_internal.cuh"
@@ -53,6 +57,8 @@ constexpr int kThr = kWarps * 32;
 constexpr int kTile = 32;                        // keys per warp and step, in two halves of 16
 constexpr int kStep = kWarps * kTile;            // keys per step
 constexpr int kUnitCost = 1;                     // steps that a unit's start and merge take as long as
+constexpr int kStages = 3;                       // tiles of a warp's ring (gathered keys)
+constexpr int kStage = 2 * kTile * kD;            // bytes: K rows, then V rows
 constexpr int kMaxParts = 512;                   // CTAs, and so parts of a unit
 constexpr float kWBias = 14.0f;                  // w is held times 2^14
 constexpr int kPart = 4 + kD;                    // floats of a partial: m, l, m2, 0, sums
@@ -126,6 +132,18 @@ __device__ __forceinline__ uint4 load_row16(const uint8_t* p, bool ok = true) {
                  : "l"(p));
   return v;
 }
+
+// cp.async that fills with zeros when !ok (nothing is read then)
+__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+
+// 16-byte chunk ch of row r of a ring's tile is stored at chunk ch ^ swz(r): the 8 lanes of a
+// load phase (two K rows 2i, 2i + 1 and four neighbouring chunks; four V rows 2i or 2i + 1
+// and two neighbouring chunks) then cover all 32 banks.
+__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r & 1) << 2); }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
@@ -500,6 +518,7 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
   constexpr bool kLo = sizeof(T) == 4;   // fp32 queries take two fp16 parts
   using S = Smem<NT>;
   __shared__ __align__(16) S sm;
+  extern __shared__ __align__(128) uint8_t ring[];   // !kUni: [kWarps][kStages][kStage]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gid = lane >> 2, q = lane & 3;
   pdl_wait();
@@ -597,71 +616,46 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
   QueryRow<T> qrow;
   qrow.load(a.q, (int64_t(pf.b) * a.U + pf.j) * a.G + head, head_ok, q);
 
-  // ---- loads.  Half u of a tile: kreg[u][2 tau + j] is key 8 tau + gid, bytes 16 (4 j + q);
-  // vreg[u][i] key 8 (i / 2) + 2 q + i % 2, bytes 16 gid.  kSc: scales of a half that a lane needs
+  // ---- loads.  kUni: straight into registers; half u of a tile: kreg[u][2 tau + j] is key
+  // 8 tau + gid, bytes 16 (4 j + q); vreg[u][i] key 8 (i / 2) + 2 q + i % 2, bytes 16 gid.
+  // kSc: scales of a half that a lane needs.
   constexpr int kSc = kUni ? 1 : 4;
-  uint4 kreg[2][4], vreg[2][4];
-  float ks_in[2][kSc], vs_in[2][kSc];
+  uint4 kreg[kUni ? 2 : 1][4], vreg[2][4];
+  float ks_in[2], vs_in[2];
   const auto load_k_of = [&](const Rows& r, auto full) {
-    constexpr bool kFull = decltype(full)::value;
-    // both scales with the keys: they are needed together, before the values
+    [[maybe_unused]] constexpr bool kFull = decltype(full)::value;
+    if constexpr (kUni) {
+      // both scales with the keys: they are needed together, before the values
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if constexpr (kUni) {
+      for (int u = 0; u < 2; ++u) {
         const bool some = kFull || ((r.mask >> (16 * u)) & 0xffffu) != 0;
-        ks_in[u][0] = some ? __ldg(a.c.ks + (r.row[u] >> a.c.bshift)) : 0.0f;
-        vs_in[u][0] = some ? __ldg(a.c.vs + (r.row[u] >> a.c.bshift)) : 0.0f;
+        ks_in[u] = some ? __ldg(a.c.ks + (r.row[u] >> a.c.bshift)) : 0.0f;
+        vs_in[u] = some ? __ldg(a.c.vs + (r.row[u] >> a.c.bshift)) : 0.0f;
       }
-    }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      [[maybe_unused]] const uint32_t there = r.mask >> (16 * u);
-      if constexpr (kUni) {
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t there = r.mask >> (16 * u);
         const uint8_t* const p = a.c.k + int64_t(r.row[u]) * kD + gid * kD + 16 * q;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          kreg[u][i] = load_row16(p + (i >> 1) * 8 * kD + (i & 1) * 64,
-                                  kFull || ((there >> (8 * (i >> 1) + gid)) & 1u));
-      } else {
-#pragma unroll
-        for (int tau = 0; tau < 2; ++tau) {
-          const int row = __shfl_sync(0xffffffffu, r.row[0], 16 * u + 8 * tau + gid);
-          const uint8_t* const p = a.c.k + int64_t(row) * kD + 16 * q;
-          kreg[u][2 * tau] = load_row16(p, kFull || row >= 0);
-          kreg[u][2 * tau + 1] = load_row16(p + 64, kFull || row >= 0);
-        }
-        if (u == 1) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            ks_in[i >> 2][kUni ? 0 : i & 3] = __shfl_sync(
-                0xffffffffu, r.ks, 16 * (i >> 2) + 8 * ((i >> 1) & 1) + 2 * q + (i & 1));
-        }
+          kreg[kUni ? u : 0][i] =
+              load_row16(p + (i >> 1) * 8 * kD + (i & 1) * 64,
+                         kFull || ((there >> (8 * (i >> 1) + gid)) & 1u));
       }
     }
   };
   const auto load_v_of = [&](const Rows& r, auto full) {
-    constexpr bool kFull = decltype(full)::value;
+    [[maybe_unused]] constexpr bool kFull = decltype(full)::value;
+    if constexpr (kUni) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      [[maybe_unused]] const uint32_t there = r.mask >> (16 * u);
-      if constexpr (kUni) {
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t there = r.mask >> (16 * u);
         const uint8_t* const p = a.c.v + int64_t(r.row[u]) * kD + 2 * q * kD + 16 * gid;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          vreg[u][i] = load_row16(p + (i >> 1) * 8 * kD + (i & 1) * kD,
-                                  kFull || ((there >> (8 * (i >> 1) + 2 * q + (i & 1))) & 1u));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = __shfl_sync(0xffffffffu, r.row[0], 16 * u + 8 * (i >> 1) + 2 * q + (i & 1));
-          vreg[u][i] = load_row16(a.c.v + int64_t(row) * kD + 16 * gid, kFull || row >= 0);
-        }
-        if (u == 1) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            vs_in[i >> 2][kUni ? 0 : i & 3] = __shfl_sync(
-                0xffffffffu, r.vs, 16 * (i >> 2) + 8 * ((i >> 1) & 1) + 2 * q + (i & 1));
-        }
+          vreg[u][i] = load_row16(
+              p + (i >> 1) * 8 * kD + (i & 1) * kD,
+              kFull || ((there >> (8 * (i >> 1) + 2 * q + (i & 1))) & 1u));
       }
     }
   };
@@ -673,17 +667,35 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
     if (r.mask == 0xffffffffu) load_v_of(r, std::true_type{});
     else load_v_of(r, std::false_type{});
   };
-  // lane i pulls key i's K and V rows (one 128-byte line each) into L2
-  const auto pull = [&](const Rows& r) {
-    const int row = kUni ? (lane < 16 ? r.row[0] : r.row[1] - 16) + lane : r.row[0];
-    if ((r.mask >> lane) & 1u) {
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.k + int64_t(row) * kD));
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.v + int64_t(row) * kD));
+  // kUni: lane i pulls key i's K and V rows (one 128-byte line each) into L2.  Else the rows are
+  // copied into stage st of the ring, 8 lanes to a row.
+  const auto request = [&](const Rows& r, [[maybe_unused]] int st) {
+    if constexpr (kUni) {
+      const int row = (lane < 16 ? r.row[0] : r.row[1] - 16) + lane;
+      if ((r.mask >> lane) & 1u) {
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.k + int64_t(row) * kD));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.v + int64_t(row) * kD));
+      }
+    } else {
+      __syncwarp();   // the stage has been read by every lane
+      if (r.mask != 0u) {
+        const uint32_t base = smem_addr(ring + (warp * kStages + st) * kStage);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int n = 4 * i + (lane >> 3);
+          const int row = __shfl_sync(0xffffffffu, r.row[0], n);
+          const int64_t off = int64_t(max(row, 0)) * kD + 16 * (lane & 7);
+          const uint32_t dst = base + n * kD + 16 * ((lane & 7) ^ swz(n));
+          cp_async_16_or_zero(dst, a.c.k + off, row >= 0);
+          cp_async_16_or_zero(dst + kTile * kD, a.c.v + off, row >= 0);
+        }
+      }
+      cp_async_commit();
     }
   };
 
-  // Tiles under way: r0 in registers (or coming), r1 the next one, tb with its pages and ta with
-  // its positions coming.
+  // Tiles under way: r0 in registers or in the ring (or coming), r1 the next one (pulled into L2,
+  // or on its way into the ring), tb with its pages and ta with its positions coming.
   Place cur = pf;
   int placed = v;   // place of pf's step
   const auto next_tile = [&]() {
@@ -704,12 +716,14 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
     r0 = tile_rows<kUni>(a, t0);
     load_k(r0);
     load_v(r0);
+    if (!kUni) request(r0, 0);
     r1 = tile_rows<kUni>(a, t1);
-    pull(r1);
+    request(r1, 1);
   }
+  int st = 0;   // r0's stage of the ring
   const auto fetch = [&]() {
     const Rows r = tile_rows<kUni>(a, tb);
-    pull(r);
+    request(r, st == 0 ? kStages - 1 : st - 1);
     tb = ta;
     tile_pages<kUni>(a, tb);
     ta = next_tile();
@@ -744,12 +758,18 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
       };
       // ---- scores x (before scaling) of keys 16 u + 8 tau + 2 q + {0, 1}
       float x[2][4], sf[2][kSc], ksc[2][kSc], vsc[2][kSc];
+      [[maybe_unused]] const uint8_t* const tile = ring + (warp * kStages + st) * kStage;
+      if constexpr (!kUni) {
+        cp_async_wait_pending(1);
+        __syncwarp();
+      }
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int i = 0; i < kSc; ++i) {
-          ksc[u][i] = ks_in[u][i];
-          vsc[u][i] = vs_in[u][i];
+          const int from = 16 * u + 8 * (i >> 1) + 2 * q + (i & 1);
+          ksc[u][i] = kUni ? ks_in[u] : __shfl_sync(0xffffffffu, r0.ks, from);
+          vsc[u][i] = kUni ? vs_in[u] : __shfl_sync(0xffffffffu, r0.vs, from);
         }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -758,7 +778,10 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
           float cc[2][4];   // two chains: dimensions 0..63 and 64..127
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint4 w = kreg[u][2 * tau + j];
+            const int n = 16 * u + 8 * tau + gid;
+            const uint4 w = kUni ? kreg[kUni ? u : 0][2 * tau + j]
+                                 : *reinterpret_cast<const uint4*>(
+                                       tile + n * kD + 16 * ((4 * j + q) ^ swz(n)));
             const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -859,6 +882,16 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
       // A tile's product is formed by itself and added in fp32: the tensor cores' own sums drop
       // bits below the sum's last, always towards zero, which over thousands of keys shows (2.1e-6
       // of the result at 128K keys per head against 1.0e-6 of fp32 sums).
+      if constexpr (!kUni) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int n = 16 * u + 8 * (i >> 1) + 2 * q + (i & 1);
+            vreg[u][i] =
+                *reinterpret_cast<const uint4*>(tile + (kTile + n) * kD + 16 * (gid ^ swz(n)));
+          }
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -905,6 +938,7 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
     }
     r0 = r1;
     r1 = r2;
+    if (!kUni) st = st + 1 == kStages ? 0 : st + 1;
 
     const int u0 = v - cur.ls;                  // the place of the unit's first step
     const int unit_end = u0 + cur.ns;
@@ -1150,9 +1184,17 @@ Room workspace_room(int B, int Hq, int Hkv, int64_t Lmax, int k, bool shared, bo
 
 template <typename T, int FMT, int NT>
 cudaError_t run_attention(const Args& a, int ctas, bool uni, cudaStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  const auto given = kv8_attention_kernel<T, FMT, NT, false>;
+  if (!uni) {
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(given),
+                                     kWarps * kStages * kStage, done, false);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas));
   cfg.blockDim = dim3(kThr);
+  cfg.dynamicSmemBytes = uni ? 0 : kWarps * kStages * kStage;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1160,7 +1202,7 @@ cudaError_t run_attention(const Args& a, int ctas, bool uni, cudaStream_t stream
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return uni ? cudaLaunchKernelEx(&cfg, kv8_attention_kernel<T, FMT, NT, true>, a)
-             : cudaLaunchKernelEx(&cfg, kv8_attention_kernel<T, FMT, NT, false>, a);
+             : cudaLaunchKernelEx(&cfg, given, a);
 }
 
 template <typename T, int FMT>
