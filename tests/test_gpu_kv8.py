@@ -421,6 +421,39 @@ def test_sparse_over_several_weight_slices():
     _check_sparse(c, c.upload(ad), _q(1, 4, torch.bfloat16, 3), idx, False, inplace=False)
 
 
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_sparse_weights_of_many_long_sequences(shared, inplace):
+    """Enough slices to fill the device are taken wide: the sums of 76 sequences at once are those
+    of 19 at a time, bit for bit (lists of one step: the attention's own results do not differ)."""
+    B, L, Hq, k = 76, 8300, 4, 100
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kv = [torch.randint(-127, 128, (B, 2, L + 20, D), generator=g, device="cuda").to(torch.int8)
+          for _ in range(2)]
+    sc = torch.exp2(torch.randint(-9, -6, (B, 2, (L + 20) // 16), generator=g, device="cuda").float())
+    q = torch.randn((B, Hq, D), generator=g, device="cuda").bfloat16()
+    idx = torch.from_numpy(_lists(np.random.default_rng(4), B, 2 if shared else Hq, L, k, drop=0.1)).int().cuda()
+    w0 = torch.rand((B, 2, L + 20), generator=g, device="cuda")
+
+    def run(s):
+        cache = ad.KV8Cache(kv[0][s], kv[1][s], sc[s], sc[s], 16)
+        n = q[s].shape[0]
+        ws = ad.kv8_sparse_attention_workspace(n, Hq, 2, k, shared=shared, weights=True)
+        w, start = torch.full_like(w0[s], 5.0), w0[s].clone()
+        out = ad.kv8_sparse_attention(q[s], cache, idx[s], ws, shared=shared, weights=start,
+                                      **({} if inplace else dict(weights_out=w)))
+        fine(ws)
+        return out, start if inplace else w
+
+    out, w = run(slice(0, B))
+    for b in range(0, B, 19):
+        o, ww = run(slice(b, b + 19))
+        assert torch.equal(out[b:b + 19], o) and torch.equal(w[b:b + 19], ww)
+    heads = (idx >= 0).any(-1).double().sum(1) * (Hq // 2 if shared else 1)
+    # each weight is off by a few 2^-24 of itself, and the running sum (below 5) rounds once per place
+    assert torch.allclose((w.double() - w0.double()).sum((1, 2)), heads, rtol=0, atol=2 * Hq * k * 2.0 ** -22)
+
+
 def test_sparse_positions_out_of_range_are_recorded():
     c = Case(1, 1, 64, "e4m3", block=16, seed=7)
     cache, q = c.upload(ad), _q(1, 1, torch.bfloat16)

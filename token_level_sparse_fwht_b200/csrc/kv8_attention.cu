@@ -1078,9 +1078,14 @@ __global__ void __launch_bounds__(256) kv8_weights_kernel(
 // lists of its heads one after another, adding the weights that fall into its slice in
 // shared memory; a list without repeats adds at most once per position and head, so the
 // order of the sums does not depend on timing.
-constexpr int kSlice = 4096;
+// Every slice reads the whole lists, so slices are wide (and the old sums requested before the
+// lists, their latency being in the way then) when they still fill the device, and narrow
+// otherwise: 8 sequences of 32K, 8 kv heads, 4 lists of 1024 each take 9.0 us wide against 10.8 narrow;
+// one sequence 4.8 against 4.2.
+constexpr int kWideSlice = 8192, kNarrowSlice = 4096;
 
-__global__ void __launch_bounds__(512) kv8_sparse_weights_kernel(
+template <int kSlice>
+__global__ void __launch_bounds__(512, kSlice == kWideSlice ? 2 : 1) kv8_sparse_weights_kernel(
     const int32_t* __restrict__ idx, int k, const float* __restrict__ scores,
     int64_t score_stride, const float* __restrict__ stats, int lists, int G, int64_t Lmax,
     int slices, const float* w_in, float* w_out) {
@@ -1111,6 +1116,15 @@ __global__ void __launch_bounds__(512) kv8_sparse_weights_kernel(
     }
   };
   load(0, 0, pos, x);
+  const float* const in = w_in + unit * Lmax + base;
+  float* const out = w_out + unit * Lmax + base;
+  constexpr bool kEarly = kSlice == kWideSlice;
+  [[maybe_unused]] float old[kSlice / 512];
+  if (kEarly && in != out) {
+#pragma unroll
+    for (int u = 0; u < kSlice / 512; ++u)
+      if (tid + u * 512 < n) old[u] = __ldg(in + tid + u * 512);
+  }
   for (int i = tid; i < n; i += 512) sum[i] = 0.0f;
   __syncthreads();
   for (int li = 0, i0 = 0; li < lists;) {
@@ -1138,11 +1152,13 @@ __global__ void __launch_bounds__(512) kv8_sparse_weights_kernel(
       x[u] = next_x[u];
     }
   }
-  const float* const in = w_in + unit * Lmax + base;
-  float* const out = w_out + unit * Lmax + base;
   if (in == out) {
     for (int i = tid; i < n; i += 512)
       if (sum[i] != 0.0f) out[i] = in[i] + sum[i];
+  } else if constexpr (kEarly) {
+#pragma unroll
+    for (int u = 0; u < kSlice / 512; ++u)
+      if (tid + u * 512 < n) out[tid + u * 512] = old[u] + sum[tid + u * 512];
   } else {
 #pragma unroll 8
     for (int i = tid; i < n; i += 512) out[i] = __ldg(in + i) + sum[i];
@@ -1282,11 +1298,14 @@ cudaError_t launch_kv8_attention(const Kv8& c, int fmt, const void* q, adamas_dt
                               a.score_stride, static_cast<const float*>(a.stats), seq_lens, c.Hkv,
                               G, c.Lmax, int(tiles), w_in, w_out, a.err);
   }
-  const int64_t slices = (c.Lmax + kSlice - 1) / kSlice;
+  const bool wide = units * ((c.Lmax + kWideSlice - 1) / kWideSlice) >= device_sms();
+  const int64_t slice = wide ? kWideSlice : kNarrowSlice;
+  const int64_t slices = (c.Lmax + slice - 1) / slice;
   if (units * slices > INT32_MAX) return cudaErrorNotSupported;   // more blocks than a grid holds
   cfg.gridDim = dim3(unsigned(units * slices));
   cfg.blockDim = dim3(512);
-  return cudaLaunchKernelEx(&cfg, kv8_sparse_weights_kernel, idx, k,
+  return cudaLaunchKernelEx(&cfg, wide ? kv8_sparse_weights_kernel<kWideSlice>
+                                       : kv8_sparse_weights_kernel<kNarrowSlice>, idx, k,
                             static_cast<const float*>(a.scores), a.score_stride,
                             static_cast<const float*>(a.stats), shared ? 1 : G, G, c.Lmax,
                             int(slices), w_in, w_out);
