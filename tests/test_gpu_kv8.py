@@ -59,6 +59,19 @@ def test_read_every_byte_and_outside_positions():
         ad.check_workspace(ws)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("e", [-110, 95, 106])
+def test_read_of_very_large_and_very_small_scales(fmt, e):
+    c = Case(1, 2, 130, fmt, block=16, seed=2)
+    c.ks, c.vs = c.ks * 2.0 ** e, c.vs * 2.0 ** e
+    ws = ad.kv8_workspace()
+    got = ad.kv8_read(c.upload(ad), 0, 130, ws, dtype=torch.float32)
+    fine(ws)
+    for g, want in zip(got, c.values()):
+        assert np.abs(want).max() < 2.0 ** 127
+        assert np.array_equal(g.double().cpu().numpy(), want[:, :, :130])
+
+
 # ----------------------------------------------------------------------- append
 def _append_case(fmt, dtype, block, page, B, Hkv, L, starts, counts, n, seed, layout="bhnd", codes=None):
     c = Case(B, Hkv, L, fmt, block=block, page=page, seed=seed, codes=codes is not None)
@@ -297,6 +310,15 @@ def test_dense_scales_of_another_quantiser_and_extreme_spread(fmt):
     _check_dense(c, c.upload(ad), _q(1, 2, torch.float32, 6, amp=2.0 ** -40), [64])
     c.vs = np.full_like(c.vs, 2.0 ** -120)            # every value tiny
     _check_dense(c, c.upload(ad), _q(1, 2, torch.float32, 6, amp=2.0 ** -40), [64])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("e", [-100, 100])
+@pytest.mark.parametrize("block", [4, 16])
+def test_dense_very_large_and_very_small_values(fmt, e, block):
+    c = Case(2, 2, 300, fmt, block=block, seed=3)
+    c.vs = c.vs * 2.0 ** e
+    _check_dense(c, c.upload(ad), _q(2, 8, torch.bfloat16, 5), [300, 41], weights=True)
 
 
 def test_dense_dead_rows_may_hold_anything():

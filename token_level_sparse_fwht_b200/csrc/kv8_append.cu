@@ -385,7 +385,8 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(
   };
   uint32_t odd = 0;
 #pragma unroll
-  for (int u = 0; u < kReadPer; ++u) odd |= __float_as_uint(s[u]) & 0x7fffffu;
+  for (int u = 0; u < kReadPer; ++u)
+    odd |= (__float_as_uint(s[u]) & 0x7fffffu) | uint32_t(fabsf(s[u]) > kLargestShifted);
   if (odd == 0) write(std::true_type{});
   else write(std::false_type{});
 }

@@ -165,7 +165,9 @@ __device__ __forceinline__ uint32_t pack8_scaled(float a, float b, float c, floa
 }
 
 // Four bytes times a scale (v * s rounded once).  int8: the biased byte in the last place of 2^23
-// is a float; for a power of two s its offset leaves in the same fused multiply-add, exactly.
+// is a float; for a power of two s its offset leaves in the same fused multiply-add, exactly
+// (kPow2; s at most kLargestShifted, so that the offset times s is finite).
+constexpr float kLargestShifted = 0x1p100f;
 template <int FMT, bool kPow2>
 __device__ __forceinline__ void scaled8(uint32_t w, float s, float v[4]) {
   if constexpr (FMT == kFmtE4m3) {
