@@ -529,7 +529,8 @@ typedef struct {
  * after starts[b] + counts[b] keep their bytes.  With cache->codes the new keys' codes
  * are written too, from the rows as given: ratio = 0 uses the fixed threshold t,
  * 0 < ratio <= 1 per-vector thresholds (adamas_encode_keys_absmax).  A sequence whose
- * start or count is out of range is left alone.  ws: at least 256 bytes.
+ * start or count is out of range is left alone.  Sequences may share pages, but not one
+ * that two of them append to.  ws: at least 256 bytes.
  */
 adamas_status adamas_kv8_append(const adamas_kv8_cache* cache, const void* k_new,
                                 const void* v_new, adamas_dtype dt, int64_t n_new,
@@ -561,8 +562,8 @@ adamas_status adamas_kv8_read(const adamas_kv8_cache* cache, const int32_t* star
  * required with it.
  *
  * The workspace (adamas_kv8_attention_workspace_bytes, weights 0 or 1) is zero-filled
- * once (adamas_workspace_init); each call leaves its counters at zero.  Calls that may
- * run at the same time need one workspace each.
+ * once (adamas_workspace_init): its error word stays, the rest is scratch of one call.
+ * Calls that may run at the same time need one workspace each.
  */
 size_t adamas_kv8_attention_workspace_bytes(int B, int Hq, int Hkv, int d, int64_t Lmax,
                                             int weights);
@@ -612,7 +613,8 @@ adamas_status adamas_evict_select(const float* weights, int B, int Hkv, int64_t 
  * row_bytes (32, 256 or 512: codes, bf16 or fp32 rows) in the cache layouts of
  * adamas_decode_step (page_size = 0) or adamas_decode_step_paged.  dst may equal src
  * (the move is then done in place; keep must be ascending); otherwise they must not
- * overlap.  keep as written by adamas_evict_select for the same seq_lens.
+ * overlap.  keep as written by adamas_evict_select for the same seq_lens.  In a paged
+ * buffer no two sequences may share a page that receives rows.
  */
 adamas_status adamas_compact_rows(const void* src, void* dst, int row_bytes, int B, int Hkv,
                                   int64_t Lmax, int page_size, int64_t num_pages,
@@ -627,7 +629,10 @@ adamas_status adamas_compact_rows(const void* src, void* dst, int row_bytes, int
  * the kept values.  A block in place whose rows all stay where they are keeps bytes and
  * scale.  lens_out[b] = min(seq_lens[b], budget) (lens_out may equal seq_lens).  dst may be
  * the same cache (in place) or one that shares no memory with src, of the same format,
- * B and Hkv, with dst->Lmax >= budget.  weights_out is [B][Hkv][dst->Lmax].
+ * B and Hkv, with dst->Lmax >= budget.  weights_out is [B][Hkv][dst->Lmax].  No two
+ * sequences of dst may share a page that receives rows; in place that is every page of
+ * the first `budget` positions, so a prefix that sequences share has to be evicted into
+ * another cache.
  */
 adamas_status adamas_kv8_evict(const adamas_kv8_cache* src, const adamas_kv8_cache* dst,
                                const float* weights_in, float* weights_out,

@@ -246,6 +246,23 @@ def test_evict_select_and_compact_refusals():
         assert g(*a) == ERR_INVALID_ARG, (i, bad)
 
 
+def test_buffers_that_overlap_in_part_are_refused():
+    far = dict(k=A + (1 << 24), v=A + (1 << 25), k_scale=A + (1 << 26), v_scale=A + (1 << 27))
+    rows = 2 * 8 * 4096
+    for kw in (dict(k=A + 128 * (rows - 1)), dict(v=A + 4096), dict(k_scale=A + 256), dict(v_scale=A + 128 * rows - 4)):
+        assert _evict(cache(), dst=cache(**{**far, **kw})) == ERR_INVALID_ARG, kw
+    n = 2 * 8 * 4096 * 4
+    assert _evict(cache(), dst=cache(), w_in=A, w_out=A + n - 4) == ERR_INVALID_ARG
+    for att in (_dense, _sparse):
+        assert att(cache(), w_in=A, w_out=A + n - 4, wb=1 << 40) == ERR_INVALID_ARG
+    f = ad.lib().adamas_evict_select
+    assert f(A, 2, 8, 4096, A, 1000, 4, 100, A, A + 4096, 2048, A, 256, None) == ERR_INVALID_ARG
+    g = ad.lib().adamas_compact_rows
+    assert g(A, A + 256 * (rows - 1), 256, 2, 8, 4096, 0, 0, None, 0, A, 1000, A, A, 256, None) == ERR_INVALID_ARG
+    # paged: as many rows as there are pages
+    assert g(A, A + 256 * 31, 256, 2, 1, 32, 16, 2, A, 2, A, 10, A, A, 256, None) == ERR_INVALID_ARG
+
+
 # ----------------------------------------------------------------------- binding
 def test_binding_refuses_host_tensors_and_wrong_shapes():
     k = torch.zeros((1, 2, 64, 128), dtype=torch.int8)

@@ -95,6 +95,37 @@ adamas_status check_cache(const adamas_kv8_cache* p, Kv8& c) {
   return ADAMAS_OK;
 }
 
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Range& x, const Range& y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  return x.p && y.p && a < b + y.bytes && b < a + x.bytes;
+}
+// Rows of a layout's buffer.
+size_t buffer_rows(const Kv8& c) {
+  return c.table ? size_t(c.num_pages) * size_t(c.Hkv) << c.page_shift
+                 : size_t(c.B) * size_t(c.Hkv) * size_t(c.Lmax);
+}
+bool caches_overlap(const Kv8& a, const Kv8& b) {
+  const auto ranges = [](const Kv8& c, Range (&r)[5]) {
+    const size_t n = buffer_rows(c), blocks = n >> c.bshift;
+    r[0] = {c.k, n * kD};
+    r[1] = {c.v, n * kD};
+    r[2] = {c.ks, blocks * 4};
+    r[3] = {c.vs, blocks * 4};
+    r[4] = {c.codes, n * kCodeBytes};
+  };
+  Range ra[5], rb[5];
+  ranges(a, ra);
+  ranges(b, rb);
+  for (const Range& x : ra)
+    for (const Range& y : rb)
+      if (overlap(x, y)) return true;
+  return false;
+}
+
 bool good_ws(const void* ws, size_t bytes, size_t need) {
   return ws != nullptr && aligned(ws, 256) && bytes >= need;
 }
@@ -112,10 +143,10 @@ adamas_status check_weights(const float* in, const float* out) {
   return in && aligned(in, 4) && aligned(out, 4) ? ADAMAS_OK : ADAMAS_ERR_INVALID_ARG;
 }
 
-// Workspace sizes also answer for arguments that no call accepts: 0.
 // A call's 128-key steps are counted in 32 bits.
 bool few_steps(int64_t units, int64_t n) { return units * ((n + 127) / 128) <= INT32_MAX / 2; }
 
+// Workspace sizes also answer for arguments that no call accepts: 0.
 adamas_status check_attention_sizes(int B, int Hq, int Hkv, int d, int64_t n) {
   if (B <= 0 || n <= 0) return ADAMAS_ERR_INVALID_ARG;
   const adamas_status s = check_heads(Hq, Hkv);
@@ -138,6 +169,8 @@ adamas_status attention_common(const void* q, adamas_dtype dt, const adamas_kv8_
   if (!few_steps(int64_t(c.B) * Hq, idx ? k : c.Lmax)) return ADAMAS_ERR_UNSUPPORTED;
   s = check_weights(w_in, w_out);
   if (s != ADAMAS_OK) return s;
+  const size_t w_bytes = size_t(c.B) * size_t(c.Hkv) * size_t(c.Lmax) * 4;
+  if (w_in != w_out && overlap({w_in, w_bytes}, {w_out, w_bytes})) return ADAMAS_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(seq_lens, 4) || !aligned(idx, 4))
     return ADAMAS_ERR_INVALID_ARG;
   if (!good_ws(ws, ws_bytes,
@@ -241,6 +274,10 @@ adamas_status adamas_evict_select(const float* weights, int B, int Hkv, int64_t 
   if (weights_out && (Lmax_out < budget || Lmax_out > kMaxLen || !aligned(weights_out, 4) ||
                       (weights_out == weights && Lmax_out != Lmax)))
     return ADAMAS_ERR_INVALID_ARG;
+  const size_t units = size_t(B) * size_t(Hkv);
+  if (weights_out != weights && overlap({weights, units * size_t(Lmax) * 4},
+                                        {weights_out, units * size_t(Lmax_out) * 4}))
+    return ADAMAS_ERR_INVALID_ARG;
   if (!aligned(weights, 4) || !aligned(seq_lens, 4) || !aligned(keep, 4) ||
       !good_ws(workspace, ws_bytes, 256))
     return ADAMAS_ERR_INVALID_ARG;
@@ -261,6 +298,8 @@ adamas_status adamas_compact_rows(const void* src, void* dst, int row_bytes, int
                                        max_blocks_per_seq, c);
   if (s != ADAMAS_OK) return s;
   if (n_keep <= 0 || n_keep > Lmax) return ADAMAS_ERR_INVALID_ARG;
+  const size_t bytes = buffer_rows(c) * size_t(row_bytes);
+  if (src != dst && overlap({src, bytes}, {dst, bytes})) return ADAMAS_ERR_INVALID_ARG;
   if (!aligned(src, 16) || !aligned(dst, 16) || !aligned(keep, 4) || !aligned(seq_lens, 4) ||
       !good_ws(workspace, ws_bytes, 256))
     return ADAMAS_ERR_INVALID_ARG;
@@ -286,6 +325,7 @@ adamas_status adamas_kv8_evict(const adamas_kv8_cache* src, const adamas_kv8_cac
   const bool k = a.k == b.k, v = a.v == b.v, ks = a.ks == b.ks, vs = a.vs == b.vs;
   if (k != v || k != ks || k != vs || (b.codes && (a.codes == b.codes) != k))
     return ADAMAS_ERR_INVALID_ARG;
+  if (!k && caches_overlap(a, b)) return ADAMAS_ERR_INVALID_ARG;
   if (k && (a.Lmax != b.Lmax || a.table != b.table || a.num_pages != b.num_pages ||
             a.page_shift != b.page_shift || a.max_blocks != b.max_blocks || a.bshift != b.bshift ||
             a.codes != b.codes))
