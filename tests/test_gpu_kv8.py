@@ -283,6 +283,20 @@ def test_dense_many_short_sequences():
     _check_dense(c, c.upload(ad, max_seq_len=200), _q(150, 16, torch.bfloat16, 3), lens, weights=True)
 
 
+@pytest.mark.parametrize("G,at", [(1, 0), (3, 17), (8, 39)])
+def test_dense_one_long_sequence_among_short_ones(G, at):
+    lens = [int(x) for x in np.random.default_rng(G).integers(0, 60, 40)]
+    lens[at] = 4000
+    c = Case(40, 1, 4000, "int8", block=16, seed=G)
+    _check_dense(c, c.upload(ad), _q(40, G, torch.bfloat16, 7), lens, weights=True)
+
+
+@pytest.mark.parametrize("L", [128 * 8, 128 * 8 + 1, 128 * 9 + 1, 128 * 10])
+def test_dense_units_of_few_and_of_many_parts(L):
+    c = Case(1, 3, L, "e4m3", block=64, seed=8)
+    _check_dense(c, c.upload(ad), _q(1, 24, torch.bfloat16, 7), [L], weights=True)
+
+
 def test_dense_all_sequences_empty():
     c = Case(3, 2, 64, "e4m3")
     out = _check_dense(c, c.upload(ad), _q(3, 4, torch.bfloat16), [0, 0, 0], weights=True)

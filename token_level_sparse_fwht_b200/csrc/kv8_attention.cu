@@ -80,7 +80,8 @@ struct Args {
   float* part;              // [2 CTAs][G][kPart]
   float* stats;             // [B * Hq][2]: M, 1 / l (nullptr: not wanted)
   float* scores;            // [B * Hq][score_stride] (nullptr: not wanted)
-  int4* cuts;               // [CTAs]: the unit that ends behind this CTA: unit (2 words), parts
+  int4* cuts;               // [CTAs]: the unit that ends behind this CTA: unit (2 words), parts,
+                            // which of them this CTA's is (0: the unit begins here)
   uint32_t* err;
   int64_t score_stride;
   float scale_log2;
@@ -331,7 +332,7 @@ struct Cut {
 };
 
 // Whole units per CTA (equal units only) where that keeps 3 in 4 CTAs busy, since a unit in one piece
-// needs no second merge: 256 lists of 1024 positions on 296 CTAs take 25.6 us, cut evenly 28.1.
+// needs no second merge: 256 lists of 1024 positions on 296 CTAs take 22.0 us, cut evenly 24.6.
 // 0: cut evenly.
 __host__ __device__ inline int whole_units(int units, int steps_per_unit, int grid) {
   const int each = (units + grid - 1) / grid;
@@ -339,10 +340,13 @@ __host__ __device__ inline int whole_units(int units, int steps_per_unit, int gr
   return !few && int64_t(units) * 4 >= int64_t(each) * grid * 3 ? each : 0;
 }
 
-// Merges the parts (in CTA order) of the units that were cut: block (c, h) takes head h of the unit
-// whose first part CTA c holds, if there is one.  Thread p finds part p's factor; then warp w sums
-// parts w, w + 8, ..., 4 dimensions per lane.
-constexpr int kCombineThreads = 256;
+// Merges the parts (in CTA order) of the units that were cut; block c looks at what CTA c left.  A
+// unit of at most kFewParts parts is merged by the block of its first CTA, a warp per head; of one in more
+// (so cut into at least a first, 7 inner and a last part) the block of part h takes head h, thread p
+// finding part p's factor before warp w sums parts w, w + 8, ..., 4 dimensions per lane.  So one
+// long sequence among many short ones is not left to a warp.  (With blocks for all heads of every CTA
+// one sequence of 1000 keys took 8.4 us and one of 32K 19.6, so 7.9 and 19.4.)
+constexpr int kCombineThreads = 256, kFewParts = 8;
 
 __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(
     const int4* __restrict__ cuts, const float* __restrict__ part, int G, float* __restrict__ stats,
@@ -353,17 +357,56 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(
   __shared__ float4 sums[kW][32];
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x, h = blockIdx.y;
-  const int4 cut = cuts[c];
-  const int parts = cut.z;
-  if (parts < 2) return;
-  const int64_t unit = (int64_t(uint32_t(cut.y)) << 32) | uint32_t(cut.x);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int4 cut = cuts[blockIdx.x];
+  const int parts = cut.z;
+  const bool by_warp = parts <= kFewParts;
+  if (parts < 2 || (by_warp ? cut.w != 0 || warp >= G : cut.w >= G)) return;
+  const int h = by_warp ? warp : cut.w, c = blockIdx.x - cut.w;
+  const int64_t unit = (int64_t(uint32_t(cut.y)) << 32) | uint32_t(cut.x);
+  const auto finish = [&](float l, float M, float M2, const float4& t) {
+    const bool some = l > 0.0f || !(l == l);   // an empty list: zeros
+    const float f = some ? ex2(M2 - M - kWBias) / l : 0.0f;
+    reinterpret_cast<float4*>(out + (unit * G + h) * kD)[lane] =
+        make_float4(t.x * f, t.y * f, t.z * f, t.w * f);
+    if (stats != nullptr && lane == 0) {
+      float* const o = stats + (unit * G + h) * 2;
+      o[0] = some ? M : 0.0f;
+      o[1] = some ? 1.0f / l : 0.0f;
+    }
+  };
   // a CTA's slot 1 holds the part of a unit that begins there, slot 0 that of one that goes on
   const auto at = [&](int p) {
     return reinterpret_cast<const float4*>(
         part + (int64_t(2 * (c + p) + (p == 0 ? 1 : 0)) * G + h) * kPart);
   };
+  if (by_warp) {
+    float4 w[kFewParts], y[kFewParts];
+#pragma unroll
+    for (int p = 0; p < kFewParts; ++p) {
+      const bool ok = p < parts;
+      w[p] = ok ? __ldcg(at(p)) : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+      y[p] = ok ? __ldcg(at(p) + 1 + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float M = -INFINITY, M2 = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int p = 0; p < kFewParts; ++p) {
+      M = fmaxf(M, w[p].x);
+      M2 = fmaxf(M2, w[p].z);
+    }
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int p = 0; p < kFewParts; ++p) {
+      l += w[p].y * ref_change(w[p].x, M);
+      const float f = ref_change(w[p].z, M2);
+      t.x = fmaf(y[p].x, f, t.x);
+      t.y = fmaf(y[p].y, f, t.y);
+      t.z = fmaf(y[p].z, f, t.z);
+      t.w = fmaf(y[p].w, f, t.w);
+    }
+    finish(l, M, M2, t);
+    return;
+  }
   float4 y[kBatch];
   const auto load = [&](int p0) {
 #pragma unroll
@@ -438,78 +481,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(
     t.z += x.z;
     t.w += x.w;
   }
-  const bool some = l > 0.0f || !(l == l);
-  const float f = some ? ex2(M2 - M - kWBias) / l : 0.0f;
-  reinterpret_cast<float4*>(out + (unit * G + h) * kD)[lane] =
-      make_float4(t.x * f, t.y * f, t.z * f, t.w * f);
-  if (stats != nullptr && lane == 0) {
-    float* const o = stats + (unit * G + h) * 2;
-    o[0] = some ? M : 0.0f;
-    o[1] = some ? 1.0f / l : 0.0f;
-  }
-}
-
-// The same with one block per CTA and a warp per head, for many units (few parts each): fewer
-// blocks that find nothing to do (17 sequences, 4 kv heads with 8 query heads each: 36.2 -> 34.7 us a
-// call).
-__global__ void __launch_bounds__(kCombineThreads) kv8_combine_few_kernel(
-    const int4* __restrict__ cuts, const float* __restrict__ part, int G, float* __restrict__ stats,
-    float* __restrict__ out) {
-  constexpr int kBatch = 8;
-  pdl_wait();
-  pdl_trigger();
-  const int c = blockIdx.x, h = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4 cut = cuts[c];
-  const int parts = cut.z;
-  if (parts < 2 || h >= G) return;
-  const int64_t unit = (int64_t(uint32_t(cut.y)) << 32) | uint32_t(cut.x);
-  const auto at = [&](int p) {
-    return reinterpret_cast<const float4*>(
-        part + (int64_t(2 * (c + p) + (p == 0 ? 1 : 0)) * G + h) * kPart);
-  };
-  float4 y[kBatch], st[kBatch];
-  const auto load = [&](int p0) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const bool ok = p0 + u < parts;
-      st[u] = ok ? __ldcg(at(p0 + u)) : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
-      y[u] = ok ? __ldcg(at(p0 + u) + 1 + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  };
-  float M = -INFINITY, M2 = -INFINITY, l = 0.0f;
-  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p0 = 0; p0 < parts; p0 += kBatch) {
-    load(p0);
-    float m = M, m2 = M2;
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      m = fmaxf(m, st[u].x);
-      m2 = fmaxf(m2, st[u].z);
-    }
-    const float r = ref_change(M2, m2);
-    l *= ref_change(M, m);
-    t = make_float4(t.x * r, t.y * r, t.z * r, t.w * r);
-    M = m;
-    M2 = m2;
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      l += st[u].y * ref_change(st[u].x, M);
-      const float f = ref_change(st[u].z, M2);
-      t.x = fmaf(y[u].x, f, t.x);
-      t.y = fmaf(y[u].y, f, t.y);
-      t.z = fmaf(y[u].z, f, t.z);
-      t.w = fmaf(y[u].w, f, t.w);
-    }
-  }
-  const bool some = l > 0.0f || !(l == l);
-  const float f = some ? ex2(M2 - M - kWBias) / l : 0.0f;
-  reinterpret_cast<float4*>(out + (unit * G + h) * kD)[lane] =
-      make_float4(t.x * f, t.y * f, t.z * f, t.w * f);
-  if (stats != nullptr && lane == 0) {
-    float* const o = stats + (unit * G + h) * 2;
-    o[0] = some ? M : 0.0f;
-    o[1] = some ? 1.0f / l : 0.0f;
-  }
+  finish(l, M, M2, t);
 }
 
 // FMT: byte format; NT: value products per 16 keys (1: G <= 4, 2: G <= 8).
@@ -735,7 +707,7 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
   float m = -INFINITY, m2 = -INFINITY, l = 0.0f;
   float acc[8][4];
   bool fresh = true;
-  int4 cut_here = make_int4(0, 0, 0, 0);   // the unit that begins here and ends in a later CTA
+  int4 cut_here = make_int4(0, 0, 0, 0);   // the unit that ends in a later CTA
   for (;;) {
     const int64_t unit = int64_t(cur.b) * a.U + cur.j;
     if (fresh) {
@@ -1024,7 +996,8 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
         }
       }
       __syncthreads();   // the part is written; sums and stat are free again
-      if (parts > 1 && which == 1) cut_here = make_int4(int(unit), int(unit >> 32), parts, 0);
+      const int nth = int(blockIdx.x) - c0;
+      if (nth + 1 < parts) cut_here = make_int4(int(unit), int(unit >> 32), parts, nth);
       fresh = true;
       if (!more) break;
       v = next_v;
@@ -1276,15 +1249,11 @@ cudaError_t launch_kv8_attention(const Kv8& c, int fmt, const void* q, adamas_dt
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cuts_units(int64_t(c.B) * a.U, idx ? k : c.Lmax, idx != nullptr || seq_lens == nullptr, ctas)) {
-    // parts of a unit if all are of full length
-    const bool few = int64_t(c.B) * a.U * 8 >= ctas;
-    cfg.gridDim = dim3(unsigned(ctas), few ? 1u : unsigned(a.G));
+    cfg.gridDim = dim3(unsigned(ctas));
     cfg.blockDim = dim3(kCombineThreads);
-    e = cudaLaunchKernelEx(&cfg, few ? kv8_combine_few_kernel : kv8_combine_kernel,
-                           static_cast<const int4*>(a.cuts), static_cast<const float*>(a.part), a.G,
-                           a.stats, out);
+    e = cudaLaunchKernelEx(&cfg, kv8_combine_kernel, static_cast<const int4*>(a.cuts),
+                           static_cast<const float*>(a.part), a.G, a.stats, out);
     if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(1);
   }
   if (!weights) return cudaSuccess;
   const int64_t units = int64_t(c.B) * c.Hkv;
