@@ -1,7 +1,8 @@
 // 8-bit caches: append (quantise with block scales, optionally the key codes) and read.
 //
 // Both move bytes (256 B in, 128 B out per bf16 row and the reverse) with a handful of
-// instructions per value, so HBM bounds them at length and latency at a few rows.
+// instructions per value, so HBM bounds them at length and latency at a few rows: 32K rows of 8
+// kv heads take 33 us each way (201 MB, 6.1 TB/s), one row for each of 32 x 8 kv heads 4 us each.
 #include <type_traits>
 
 #include "kv8_internal.cuh"

@@ -42,7 +42,11 @@
 // Otherwise (given positions, small pages or blocks) rows and scales are looked up key by key, three
 // tiles ahead, and the rows come by cp.async through a ring of three tiles per warp: a tile has a
 // whole tile's time more to arrive, and a row's address is formed once instead of by every lane
-// that holds a piece of it.
+// that holds a piece of it (8 sequences x 32 lists of 1024 keys: 22 us; straight into registers 25.6).
+//
+// Measured, e4m3 and bf16 queries: 32 kv heads x 128K keys 182 us, 6.1 TB/s of the 6.55 that a copy
+// reaches; 8 kv heads x 32K keys, 4 query heads each, 19.4 us (3.5 TB/s: about 8 us go to the
+// launches, the first loads and the merges, which 1000 keys take as well: 7.9 us).
 #include <type_traits>
 
 #include "kv8_internal.cuh"
@@ -1007,6 +1011,8 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
 }
 
 // ------------------------------------------------------------- attention weights
+// The running sums' traffic (8 bytes a position) and the scores bound these passes: 32 kv heads x
+// 128K positions take 12 us, 17 ragged sequences of up to 8K and 4 kv heads 8.6 us (latency).
 // Dense: w_out[unit][j] = w_in[unit][j] + sum_g 2^(x_gj - M_g) / l_g, from the scores the
 // attention kernel left in the workspace (4 G bytes per key written and read against 128 G
 // if K were scored again).
