@@ -616,6 +616,57 @@ def test_evict_in_place_over_many_rounds():
     _check_evict(c, [9000], 7777, 0, 100, True)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("block,page", [(16, 0), (8, 16), (256, 0)])
+def test_evict_of_many_units_into_another_cache(fmt, block, page):
+    """Enough chunks that a CTA takes several: selection, codes, sums and lengths are those of the move
+    in place, values those of the definition (in place a block whose rows all stay keeps its
+    bytes; requantised, a block that holds -128 goes to twice its scale and odd bytes round)."""
+    B, H, budget = 32, 8, 1024
+    L = budget + 256
+    g = torch.Generator(device="cuda").manual_seed(block)
+    rand = lambda *s: torch.randint(0, 256, s, generator=g, device="cuda", dtype=torch.uint8)  # noqa: E731
+    lead = (B, H, L) if page == 0 else (B * L // page, H, page)
+
+    def cache(k, v, ks, vs, codes, table):
+        dt = torch.int8 if fmt == "int8" else torch.float8_e4m3fn
+        return ad.KV8Cache(k.view(dt), v.view(dt), ks, vs, block, codes=codes, block_table=table)
+
+    rows = [rand(*lead, D) for _ in range(2)]
+    if fmt == "e4m3":
+        rows = [torch.where((x & 127) == 127, x & 128, x) for x in rows]           # no NaN
+    scales = [torch.exp2(torch.randint(-6, 6, (*lead[:2], lead[2] // block), generator=g, device="cuda").float())
+              for _ in range(2)]
+    table = None if page == 0 else torch.randperm(lead[0], generator=g, device="cuda").view(B, -1).int()
+    parts = [*rows, *scales, rand(*lead, 32)]
+    w = torch.rand((B, H, L), generator=g, device="cuda")
+    lens = torch.randint(0, L + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    lens[0] = L
+    src, there = (cache(*(x.clone() for x in parts), table) for _ in range(2))
+    dst = cache(*(torch.zeros_like(x) for x in parts), table)
+    olds = ad.kv8_read(src, 0, L, ad.kv8_workspace(), dtype=torch.float32)
+    ws, out = ad.kv8_workspace(), torch.full_like(w, 7.0)
+    keep, n = ad.kv8_evict(src, w, lens, budget, ws, sink=3, recent=50, dst=dst, weights_out=out)
+    keep2, n2 = ad.kv8_evict(there, w, lens, budget, ws, sink=3, recent=50)
+    fine(ws)
+    assert torch.equal(keep, keep2) and torch.equal(n, n2)
+    live = torch.arange(budget, device="cuda") < n[:, None, None]
+    top = 448.0 if fmt == "e4m3" else 127.0
+    for got, old in zip(ad.kv8_read(dst, 0, budget, ws, dtype=torch.float32), olds):
+        v = old.gather(2, keep.clamp(min=0).long()[..., None].expand(-1, -1, -1, D)).double()
+        v = v.masked_fill(~live[..., None], 0).view(B, H, budget // block, block, D)
+        m, e = torch.frexp(v.abs().amax((-1, -2), keepdim=True) / top)
+        scale = torch.exp2((e - (m == 0.5).int()).double().clamp(min=-126))
+        x = (v / scale).float()
+        x = x.round() if fmt == "int8" else x.to(torch.float8_e4m3fn).float()
+        want = (x.double() * scale).view(B, H, budget, D)
+        assert torch.equal(got.masked_fill(~live[..., None], 0).double(), want)
+    by_position = lambda c: c.codes if page == 0 else c.codes[table.long()].transpose(1, 2).reshape(B, H, L, 32)  # noqa: E731
+    a, b = by_position(dst)[:, :, :budget], by_position(there)[:, :, :budget]
+    assert torch.equal(a * live[..., None], b * live[..., None]) and not (a * ~live[..., None]).any()
+    assert torch.equal(out[:, :, :budget].masked_fill(~live, 0), w[:, :, :budget].masked_fill(~live, 0))
+
+
 def test_evict_into_another_block_size():
     c = Case(2, 2, 500, "int8", block=8, seed=2, spread=6)
     _check_evict(c, [500, 77], 300, 0, 10, False, dst_block=32)

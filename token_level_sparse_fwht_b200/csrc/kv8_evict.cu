@@ -229,9 +229,12 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(
 }
 
 // ----------------------------------------------------------------------- moving
-// Row i of a unit comes from row keep[i] >= i (the list ascends).  Into another cache every
-// chunk of rows is a CTA's own work.  In place one cluster works on one unit's K, V or
-// codes in rounds of (cluster size) chunks, kept in registers across the cluster's barrier: when
+// Row i of a unit comes from row keep[i] >= i (the list ascends).  Into another cache the chunks of
+// rows are independent: a CTA takes up to kMoveRun of them, looks up the next one's places (list, pages)
+// while it waits for the rows of the present one, and asks the next rows into L2 before it stores
+// (16 ragged sequences x 8 heads to 6K rows, pages of 16, selection included: 102 us without runs, 90
+// with lookups ahead, 87.4 with the rows asked for; runs of 8 90.3).
+// In place one cluster works on one unit's K, V or codes in rounds of (cluster size) chunks, kept in registers across the cluster's barrier: when
 // rows [i, i + c) are written, every row below i + c has been read by every CTA that needs it, and
 // later rounds read rows at or above i + c only; so the next round is requested before this one's
 // barrier.
@@ -241,9 +244,10 @@ constexpr int kMoveThreads = 512;
 // for 16 x 8 units cut from 16K to 6K rows).
 // Rows per thread: in place every round costs a cluster barrier, so it takes more rows.  Into
 // another cache a CTA is as small as a block allows (at least 64 rows), so that few warps wait at
-// its barrier; one row per thread takes 131 us instead of 103 (the whole call), four 124.
-// Bound by the chain list -> page -> row and scale -> barrier -> store at 27 of 64 warps per SM: 128
-// units of up to 6K rows from pages of 16 take 83 us (40 % of the DRAM rate).
+// its barrier; before the runs, one row per thread took 131 us instead of 103 (the whole call), four
+// 124.  Bound by the dependent loads at up to 32 warps per SM: what is moved there, 321 MB, would take
+// 49 us at the copy rate.
+constexpr int kMoveRun = 4;
 constexpr int move_per(bool in_place) { return in_place ? 4 : 2; }
 inline int move_threads(bool in_place, int bshift) {
   return in_place ? kMoveThreads : (2 << bshift) > 128 ? 2 << bshift : 128;
@@ -255,9 +259,15 @@ struct Round {
   float s[kPer];              // -1: no row
   uint32_t stays;             // bit u: row u comes from its own place
 };
+// Where a thread's rows come from and (into another cache) go; -1: nowhere.
+template <int kPer>
+struct Spots {
+  int from[kPer], at[kPer];
+  uint32_t stays;
+};
 
 // blockIdx.x = (unit * parts + part) * cs + rank; part 0: K, 1: V, 2: codes.  In place: cs CTAs
-// (one cluster) per unit and part, each taking every cs-th chunk; else cs chunks.
+// (one cluster) per unit and part; else cs independent ones.  Each takes every cs-th chunk.
 template <int FMT, bool kInPlace>
 __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) kv8_move_kernel(
     Kv8 src, Kv8 dst, const int32_t* __restrict__ keep, int n_keep,
@@ -318,9 +328,9 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) kv8_move_kerne
   float* const to_s = part ? dst.vs : dst.ks;
   const int piece = tid & 3;
   const int bs = 1 << dst.bshift;
-  const auto load = [&](int i0, Round<kMovePer>& r) {
+  const auto locate = [&](int i0, Spots<kMovePer>& t) {
     int p[kMovePer];
-    r.stays = 0;
+    t.stays = 0;
 #pragma unroll
     for (int u = 0; u < kMovePer; ++u) {
       const int i = i0 + u * (threads / 4) + (tid >> 2);
@@ -330,32 +340,42 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) kv8_move_kerne
 #pragma unroll
     for (int u = 0; u < kMovePer; ++u) {
       const int i = i0 + u * (threads / 4) + (tid >> 2);
+      t.from[u] = t.at[u] = -1;
+      if (i >= n) continue;
+      if (!kInPlace) t.at[u] = to_rows.row(i);
+      t.from[u] = p[u] >= 0 && p[u] < src.Lmax ? from_rows.row(p[u]) : -1;
+      if (t.from[u] < 0) atomicOr(err, kErrInput);
+      if (kInPlace && p[u] == i) t.stays |= 1u << u;
+    }
+  };
+  const auto load = [&](const Spots<kMovePer>& t, Round<kMovePer>& r) {
+    r.stays = t.stays;
+#pragma unroll
+    for (int u = 0; u < kMovePer; ++u) {
       r.s[u] = -1.0f;
       r.w[u][0] = r.w[u][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (i < n) {
-        const int row = p[u] >= 0 && p[u] < src.Lmax ? from_rows.row(p[u]) : -1;
-        if (row >= 0) {
-          const uint4* const p4 = reinterpret_cast<const uint4*>(from8 + int64_t(row) * kD) + piece;
-          r.w[u][0] = p4[0];
-          r.w[u][1] = p4[4];
-          r.s[u] = from_s[row >> src.bshift];
-          if (kInPlace && p[u] == i) r.stays |= 1u << u;
-        } else {
-          atomicOr(err, kErrInput);
-        }
+      if (t.from[u] >= 0) {
+        const uint4* const p4 = reinterpret_cast<const uint4*>(from8 + int64_t(t.from[u]) * kD) + piece;
+        r.w[u][0] = p4[0];
+        r.w[u][1] = p4[4];
+        r.s[u] = from_s[t.from[u] >> src.bshift];
       }
     }
   };
   Round<kMovePer> cur, nxt;
+  Spots<kMovePer> here, ahead;
   const int stride = rows * cs;
   int buf = 0;
-  load(rank * rows, cur);
+  locate(rank * rows, here);
+  load(here, cur);
   for (int i = tid; i < rows; i += threads) {
     top[0][i] = 0u;
     if (kInPlace) same[0][i] = 0u;
   }
   __syncthreads();
-  for (int i0 = rank * rows; i0 - rank * rows < n; i0 += stride, buf ^= 1) {
+  for (int i0 = rank * rows; i0 - rank * rows * kInPlace < n; i0 += stride, buf ^= 1) {
+    const bool more = i0 - rank * rows * kInPlace + stride < n;
+    if (!kInPlace && more) locate(i0 + stride, ahead);
     // the largest magnitude of every block of this CTA's rows
 #pragma unroll
     for (int u = 0; u < kMovePer; ++u) {
@@ -380,15 +400,24 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) kv8_move_kerne
       if (kInPlace && piece == 0 && (cur.stays >> u & 1u))
         atomicAdd(&same[kInPlace ? buf : 0][r >> dst.bshift], 1u);
     }
-    const bool more = kInPlace && i0 - rank * rows + stride < n;
-    if (more) load(i0 + stride, nxt);
+    if (kInPlace && more) {
+      locate(i0 + stride, here);
+      load(here, nxt);
+    }
     if (kInPlace) cg::this_cluster().sync();   // this round's rows and scales have been read
     else __syncthreads();
     if (more)
       for (int i = tid; i < rows; i += threads) {
         top[buf ^ 1][i] = 0u;
-        same[kInPlace ? buf ^ 1 : 0][i] = 0u;
+        if (kInPlace) same[kInPlace ? buf ^ 1 : 0][i] = 0u;
       }
+    if (!kInPlace && more && piece == 0) {
+      // the next rows come into L2 meanwhile
+#pragma unroll
+      for (int u = 0; u < kMovePer; ++u)
+        if (ahead.from[u] >= 0)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(from8 + int64_t(ahead.from[u]) * kD));
+    }
 #pragma unroll
     for (int u = 0; u < kMovePer; ++u) {
       const int r = u * (threads / 4) + (tid >> 2);
@@ -398,7 +427,7 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) kv8_move_kerne
       const int first = i >> dst.bshift << dst.bshift;
       if (kInPlace && same[kInPlace ? buf : 0][r >> dst.bshift] == uint32_t(min(bs, n - first)))
         continue;
-      const int at = to_rows.row(i);
+      const int at = kInPlace ? to_rows.row(i) : here.at[u];
       if (at < 0) {
         atomicOr(err, kErrInput);
         continue;
@@ -439,9 +468,14 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) kv8_move_kerne
       o[0] = make_uint4(w[0], w[1], w[2], w[3]);
       o[4] = make_uint4(w[4], w[5], w[6], w[7]);
     }
-    if (!kInPlace) return;
+    if (!more) return;
     __syncthreads();   // the other buffers are clear, this one is read
-    cur = nxt;
+    if (kInPlace) {
+      cur = nxt;
+    } else {
+      here = ahead;
+      load(here, cur);
+    }
   }
 }
 
@@ -507,6 +541,14 @@ int move_cluster(int64_t rows, int rows_per_cta, int64_t clusters) {
   return cs;
 }
 
+// CTAs of a unit's part, moving into another cache: runs of chunks only where two waves of CTAs (8 per
+// SM) are left.
+int64_t move_ctas(int64_t chunks, int64_t units) {
+  int64_t run = units * chunks / (device_sms() * int64_t(16));
+  run = run < 1 ? 1 : run > kMoveRun ? kMoveRun : run;
+  return (chunks + run - 1) / run;
+}
+
 }  // namespace
 
 bool evict_fits(int64_t Lmax) { return Lmax <= int64_t(kMaxShare) * kMaxCluster; }
@@ -548,7 +590,7 @@ cudaError_t launch_kv8_compact(const Kv8& src, const Kv8& dst, int fmt, const in
   const int threads = move_threads(in_place, dst.bshift);
   const int rows = move_per(in_place) * threads / 4;
   const int64_t cs = in_place ? move_cluster(n_keep, rows, units * parts)
-                              : (int64_t(n_keep) + rows - 1) / rows;
+                              : move_ctas((int64_t(n_keep) + rows - 1) / rows, units * parts);
   if (units * parts * cs > INT32_MAX) return cudaErrorNotSupported;   // more blocks than a grid holds
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
