@@ -1,0 +1,68 @@
+"""8-bit caches on the GPU at the ends of their value ranges, with bad pages and at the largest sizes,
+against the float64 oracle (oracle/kv8_ref.py)."""
+import numpy as np
+import pytest
+import torch
+
+import token_level_sparse_fwht_b200 as ad
+from kv8_helpers import D, Case, attention_oracle, check
+from oracle import kv8_ref as ref
+
+pytestmark = pytest.mark.gpu
+FMTS = ["e4m3", "int8"]
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# -------------------------------------------------------------- attention: value ranges
+def _leading_zero_block(fmt, block, lead, target, scale, seed):
+    """A cache of 64 positions whose first block has zero V rows (stored with the smallest scale, or with
+    scale 0) and scores `lead` powers of two above all others; the other blocks' largest |V| is `target`
+    times 1, 1/8, ...  Returns the case and a query [1, 2, 128]."""
+    c = Case(1, 1, 64, fmt, block=block, seed=seed, spread=0)
+    top = ref.FMAX[fmt]
+    c.v[:, :, :block] = 0
+    c.vs[...] = target / top * 2.0 ** (-3.0 * (np.arange(64 // block) % 4 - 1).clip(min=0))
+    c.vs = c.vs.astype(np.float32).astype(np.float64)
+    c.vs[..., 0] = scale
+    # dimension 0 alone leads: q_0 k_0 a log2(e) / sqrt(128) = lead
+    c.k[..., 0] = 0
+    c.k[:, :, :block] = 0
+    c.k[:, :, :block, 0] = 64
+    q = np.random.default_rng(seed).standard_normal((1, 2, D)) * 0.05
+    q[..., 0] = 16
+    c.ks[..., 0] = np.float32(lead * np.sqrt(D) / (16 * 64 * np.log2(np.e)))
+    return c, torch.from_numpy(q)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("block", [4, 16])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lead", [60, 100, 111, 114, 120, 126, 150, 200])
+@pytest.mark.parametrize("form", ["dense", "sparse", "shared"])
+def test_zero_values_that_lead_leave_the_others_finite_and_right(fmt, block, dtype, lead, form):
+    """The zero block's p is 1 and its values add nothing; the others' p is about 2^-lead and their values
+    are large, so the output is theirs alone.  2^-125 is added to the bounds: fp32 results below
+    its smallest normal number (2^-126) have fewer bits."""
+    for target in (300.0, 1000.0, 1e6):
+        for scale in (2.0 ** -126, 0.0):
+            c, q = _leading_zero_block(fmt, block, lead, target, scale, seed=lead)
+            q = q.to(dtype)
+            want, tol, ww, wtol = attention_oracle(q.double().numpy(), c, lambda b, h: np.arange(64))
+            cache, w = c.upload(ad), torch.zeros((1, 1, 64), device="cuda")
+            if form == "dense":
+                ws = ad.kv8_attention_workspace(1, 2, 1, cache.Lmax, weights=True)
+                out = ad.kv8_attention(q.cuda(), cache, i32([64]), ws, weights=w)
+            else:
+                n = 1 if form == "shared" else 2
+                idx = np.random.default_rng(1).permuted(np.tile(np.arange(64), (1, n, 1)), axis=-1)
+                ws = ad.kv8_sparse_attention_workspace(1, 2, 1, 64, shared=form == "shared", weights=True)
+                out = ad.kv8_sparse_attention(q.cuda(), cache, i32(idx.tolist()), ws,
+                                              shared=form == "shared", weights=w)
+            ad.check_workspace(ws)
+            check(out, want, tol + 2.0 ** -125, (target, scale))
+            check(w, ww, wtol + 2.0 ** -125, "weights")
+            if lead <= 111:
+                assert (np.abs(want) > 2.0 ** -122).any()

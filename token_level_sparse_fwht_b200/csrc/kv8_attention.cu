@@ -828,17 +828,25 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
         m = mn;
         m2 = m2n;
       }
-      // w = 2^(x - m) c 2^(m - m2 + 14)
-      const float lift = m2 == -INFINITY ? 1.0f : ex2(m - m2 + kWBias);
+      // w = 2^(x + E - m2 + 14) (c / 2^E), E the exponent of c: formed by itself, since p and
+      // 2^(m - m2) c can each leave the range of fp32 where w does not (a block of zeros may lead by 100
+      // and more, and m2 then lies as far below m).  E is held to 126 so that 2^-E is normal.
       uint32_t b[2][NT][2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
+        float up_w[kSc], mant[kSc];
+#pragma unroll
+        for (int i = 0; i < kSc; ++i) {
+          const int e = min(max(int(__float_as_uint(vsc[u][i]) >> 23) - 127, -126), 126);
+          up_w[i] = (float(e) + kWBias) - m2;
+          mant[i] = vsc[u][i] * pow2i(-e);
+        }
         float w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float p = there(u, i) ? ex2(fmaf(x[u][i], sf[u][kUni ? 0 : i], -m)) : 0.0f;
-          l += p;
-          w[i] = p * (vsc[u][kUni ? 0 : i] * lift);
+          const float y = x[u][i], f = sf[u][kUni ? 0 : i];
+          l += there(u, i) ? ex2(fmaf(y, f, -m)) : 0.0f;
+          w[i] = there(u, i) ? ex2(fmaf(y, f, up_w[kUni ? 0 : i])) * mant[kUni ? 0 : i] : 0.0f;
         }
         b[u][0][0] = pack_f16(w[0], w[1]);
         b[u][0][1] = pack_f16(w[2], w[3]);
