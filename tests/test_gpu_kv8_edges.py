@@ -66,3 +66,22 @@ def test_zero_values_that_lead_leave_the_others_finite_and_right(fmt, block, dty
             check(w, ww, wtol + 2.0 ** -125, "weights")
             if lead <= 111:
                 assert (np.abs(want) > 2.0 ** -122).any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("e", [-126, -120, -110])
+@pytest.mark.parametrize("L,block", [(25, 1), (1000, 16), (40000, 64)])
+def test_many_keys_of_very_small_values(fmt, e, L, block):
+    """Equal scores over L keys and value scales of 2^e: outputs are normal fp32 numbers (4 2^e and more)
+    although 1 / L of the smallest scale is none.  The bound is the helper's alone."""
+    c = Case(1, 2, L, fmt, block=block, seed=L, spread=0)
+    c.v[:] = np.abs(c.v) + ref.FMAX[fmt] / 4
+    c.v[:] = np.minimum(ref.round8(c.v, fmt), ref.FMAX[fmt])
+    c.vs[:] = 2.0 ** e
+    q = torch.zeros((1, 8, D), dtype=torch.bfloat16)
+    want, tol, _, _ = attention_oracle(q.double().numpy(), c, lambda b, h: np.arange(L))
+    assert (want > 4 * 2.0 ** e).all()
+    ws = ad.kv8_attention_workspace(1, 8, 2, c.cap)
+    out = ad.kv8_attention(q.cuda(), c.upload(ad), i32([L]), ws)
+    ad.check_workspace(ws)
+    check(out, want, tol, "out")

@@ -126,6 +126,21 @@ __device__ __forceinline__ float ref_change(float from, float to) {
   return from == to ? 1.0f : ex2(from - to);
 }
 
+// What turns a head's value sum t into its output t 2^(m2 - m - 14) / l, in two factors: with small
+// value scales m2 lies up to 126 below m, and the whole factor below fp32's normal numbers although
+// t times it may not.  The second is 1 but for exponents below -100.
+struct OutScale {
+  float f, g;
+  __device__ __forceinline__ OutScale(float m, float m2, float l, bool some) {
+    const float e = m2 - m - kWBias, e1 = fmaxf(e, -100.0f);
+    f = some ? ex2(e1) / l : 0.0f;
+    g = some ? ex2(e - e1) : 0.0f;
+  }
+  __device__ __forceinline__ float4 of(float a, float b, float c, float d) const {
+    return make_float4(a * f * g, b * f * g, c * f * g, d * f * g);
+  }
+};
+
 // 16 bytes that are read once (kept out of L1); zeros if !ok (nothing is read then).
 __device__ __forceinline__ uint4 load_row16(const uint8_t* p, bool ok = true) {
   uint4 v;
@@ -370,9 +385,8 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(
   const int64_t unit = (int64_t(uint32_t(cut.y)) << 32) | uint32_t(cut.x);
   const auto finish = [&](float l, float M, float M2, const float4& t) {
     const bool some = l > 0.0f || !(l == l);   // an empty list: zeros
-    const float f = some ? ex2(M2 - M - kWBias) / l : 0.0f;
     reinterpret_cast<float4*>(out + (unit * G + h) * kD)[lane] =
-        make_float4(t.x * f, t.y * f, t.z * f, t.w * f);
+        OutScale(M, M2, l, some).of(t.x, t.y, t.z, t.w);
     if (stats != nullptr && lane == 0) {
       float* const o = stats + (unit * G + h) * 2;
       o[0] = some ? M : 0.0f;
@@ -778,8 +792,7 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
         for (int i = 0; i < kSc; ++i) sf[u][i] = ksc[u][i] * factor;
       }
       load_k(r1);
-      // ---- references.  The value scale's exponent is rounded up, and taken as at least -112
-      // so that 2^14 times its reciprocal is finite.
+      // ---- references.  The value scale's exponent is rounded up.
       float up = -INFINITY, up2 = -INFINITY;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -789,12 +802,11 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
           const float y = there(u, i) ? x[u][i] * sf[u][kUni ? 0 : i] : -INFINITY;
           half = fmaxf(half, y);
           if (!kUni)
-            up2 = fmaxf(up2, y + float(max(int(__float_as_uint(vsc[u][kUni ? 0 : i]) >> 23) - 126,
-                                           -112)));
+            up2 = fmaxf(up2, y + float(int(__float_as_uint(vsc[u][kUni ? 0 : i]) >> 23) - 126));
         }
         up = fmaxf(up, half);
         if (kUni)
-          up2 = fmaxf(up2, half + float(max(int(__float_as_uint(vsc[u][0]) >> 23) - 126, -112)));
+          up2 = fmaxf(up2, half + float(int(__float_as_uint(vsc[u][0]) >> 23) - 126));
       }
       if (a.scores != nullptr && (NT == 2 || gid < 4) && head_ok) {
         float* const o = a.scores + (unit * a.G + head) * a.score_stride + cur.ls * kStep +
@@ -992,9 +1004,8 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
         }
         if (parts == 1) {
           const bool some = hl > 0.0f || !(hl == hl);   // an empty list: zeros
-          const float f = some ? ex2(hM2 - hM - kWBias) / hl : 0.0f;
           *reinterpret_cast<float4*>(a.out + (unit * a.G + hh) * kD + d) =
-              make_float4(t[0] * f, t[1] * f, t[2] * f, t[3] * f);
+              OutScale(hM, hM2, hl, some).of(t[0], t[1], t[2], t[3]);
           if (d == 0 && a.stats != nullptr) {
             float* const o = a.stats + (unit * a.G + hh) * 2;
             o[0] = some ? hM : 0.0f;
