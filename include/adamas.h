@@ -630,7 +630,9 @@ adamas_status adamas_compact_rows(const void* src, void* dst, int row_bytes, int
  * scale.  lens_out[b] = min(seq_lens[b], budget) (lens_out may equal seq_lens).  dst may be
  * the same cache (in place) or one that shares no memory with src, of the same format,
  * B and Hkv, with dst->Lmax >= budget.  weights_out is [B][Hkv][dst->Lmax].  Rows behind
- * the kept ones keep their bytes, but those of the last kept row's block not their scale.  No two
+ * the kept ones keep their bytes, but those of the last kept row's block not their scale; so does
+ * a row left out because its page id is out of range (a block none of whose rows came
+ * keeps its scale too).  No two
  * sequences of dst may share a page that receives rows; in place that is every page of
  * the first `budget` positions, so a prefix that sequences share has to be evicted into
  * another cache.

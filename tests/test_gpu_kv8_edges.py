@@ -85,3 +85,55 @@ def test_many_keys_of_very_small_values(fmt, e, L, block):
     out = ad.kv8_attention(q.cuda(), c.upload(ad), i32([L]), ws)
     ad.check_workspace(ws)
     check(out, want, tol, "out")
+
+
+# ----------------------------------------------------------------- eviction: bad pages
+# Positions 32 .. 47 of sequence 0 are on a page that does not exist.  Kept lists whose rows from there
+# are the first of a block, in its middle and its end, several blocks, and a whole block.
+GAPS = [[*range(8), 40, *range(48, 63)],
+        [*range(7), *range(33, 42), *range(48, 56)],
+        [3, 5, 36, 37, *range(50, 70)],
+        [*range(32, 48), *range(60, 68)],
+        [*range(0, 31, 2), 47]]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("block", [1, 4, 8, 16])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("kept", GAPS)
+def test_evict_leaves_out_only_the_rows_of_a_bad_page(fmt, block, in_place, kept):
+    c = Case(2, 2, 96, fmt, block=block, page=16, seed=7, codes=True, spread=6)
+    c.codes[:] = np.random.default_rng(3).integers(0, 256, c.codes.shape, dtype=np.uint8)
+    cache = c.upload(ad)
+    cache.block_table[0, 2] = c.num_pages + 3
+    n = len(kept)
+    d, kw = c, {}
+    if not in_place:
+        d = Case(2, 2, n, fmt, block=block, page=16, seed=8, codes=True)
+        kw = dict(dst=d.upload(ad))
+    w = torch.zeros((2, 2, cache.Lmax), device="cuda")
+    w[..., kept] = 1.0
+    before, ws = d.download(kw.get("dst", cache)), ad.kv8_workspace()
+    keep, lens = ad.kv8_evict(cache, w, i32([96, 96]), n, ws, **kw)
+    with pytest.raises(ad.AdamasError) as err:
+        ad.check_workspace(ws)
+    assert err.value.status == ad.ERR_INVALID_ARG
+    assert (keep.cpu() == torch.tensor(kept)).all() and lens.tolist() == [n, n]
+    got, vals = d.download(kw.get("dst", cache)), c.values()
+    for b in range(2):
+        came = np.array([b == 1 or not 32 <= p < 48 for p in kept])
+        for h in range(2):
+            for i in (0, 2):
+                for r in range(0, n, block):
+                    rows, ok = slice(r, min(r + block, n)), came[r:min(r + block, n)]
+                    was, now = before[i][b, h, rows], got[i][b, h, rows]
+                    assert np.array_equal(now[~ok], was[~ok]), (b, h, i, r)
+                    s = got[i + 1][b, h, r // block]
+                    if not ok.any():
+                        assert s == before[i + 1][b, h, r // block]
+                        continue
+                    stored, scale = ref.requantise(vals[i // 2][b, h, np.array(kept)[rows][ok]], fmt, block)
+                    assert np.array_equal(now[ok] * s, stored * scale[0]), (b, h, i, r)
+            want = c.codes[b, h, kept]
+            want[~came] = before[4][b, h, :n][~came]
+            assert np.array_equal(got[4][b, h, :n], want)

@@ -274,7 +274,8 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) kv8_move_kerne
     const int32_t* seq_lens, int32_t* lens_out, int parts, int cs, uint32_t* err) {
   constexpr int kMovePer = move_per(kInPlace), kMaxRows = kMovePer * kMoveThreads / 4;
   const int threads = blockDim.x, rows = kMovePer * threads / 4;   // rows per CTA and round
-  __shared__ uint32_t top[2][kMaxRows];              // largest value per block of a round
+  // per block of a round: 0 if no row of it came, else the bits of the largest value plus 1
+  __shared__ uint32_t top[2][kMaxRows];
   __shared__ uint32_t same[kInPlace ? 2 : 1][kMaxRows];   // rows of the block that stay in place
   const int tid = threadIdx.x;
   const uint32_t chunk = blockIdx.x / uint32_t(cs);
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) kv8_move_kerne
         m2 = max_magnitude<FMT>(cur.w[u][j].w, m2);
       }
       const float m = __half2float(__hmax(__low2half(m2), __high2half(m2)));
-      uint32_t v = cur.s[u] != -1.0f ? __float_as_uint(finite_abs(m * cur.s[u])) : 0u;
+      uint32_t v = cur.s[u] != -1.0f ? __float_as_uint(finite_abs(m * cur.s[u])) + 1u : 0u;
       if (bs >= 8) {
         // the warp's eight rows lie in one block
         v = __reduce_max_sync(0xffffffffu, v);
@@ -422,9 +423,12 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) kv8_move_kerne
     for (int u = 0; u < kMovePer; ++u) {
       const int r = u * (threads / 4) + (tid >> 2);
       const int i = i0 + r;
-      if (cur.s[u] == -1.0f) continue;
-      // a block whose rows all stay keeps its bytes and its scale
       const int first = i >> dst.bshift << dst.bshift;
+      const bool here_first = piece == 0 && i == first;
+      const uint32_t largest = top[buf][r >> dst.bshift];
+      // a row that did not come is left out, but a block's first one writes the scale of those that did
+      if (cur.s[u] == -1.0f && !(here_first && largest != 0u)) continue;
+      // a block whose rows all stay keeps its bytes and its scale
       if (kInPlace && same[kInPlace ? buf : 0][r >> dst.bshift] == uint32_t(min(bs, n - first)))
         continue;
       const int at = kInPlace ? to_rows.row(i) : here.at[u];
@@ -433,9 +437,10 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) kv8_move_kerne
         continue;
       }
       bool odd_ratio = false;
-      const int e = scale_exponent<FMT>(__uint_as_float(top[buf][r >> dst.bshift]));
+      const int e = scale_exponent<FMT>(__uint_as_float(largest - 1u));
       const float s = pow2i(e);
-      if (piece == 0 && i == first) to_s[at >> dst.bshift] = s;
+      if (here_first) to_s[at >> dst.bshift] = s;
+      if (cur.s[u] == -1.0f) continue;
       uint32_t w[8] = {cur.w[u][0].x, cur.w[u][0].y, cur.w[u][0].z, cur.w[u][0].w,
                        cur.w[u][1].x, cur.w[u][1].y, cur.w[u][1].z, cur.w[u][1].w};
       if (cur.s[u] != s) {
