@@ -137,3 +137,40 @@ def test_evict_leaves_out_only_the_rows_of_a_bad_page(fmt, block, in_place, kept
             want = c.codes[b, h, kept]
             want[~came] = before[4][b, h, :n][~came]
             assert np.array_equal(got[4][b, h, :n], want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("block", [4, 16])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_keeps_values_at_fp32s_largest(fmt, dtype, block, in_place):
+    """Appended values next to the type's largest are rounded up to 2^128, which the bytes and the scale hold and
+    fp32 does not; the move keeps them, and what shares their block."""
+    L = 64
+    x = np.random.default_rng(block).standard_normal((1, 2, L, D)) * 2.0 ** 118
+    x = torch.from_numpy(x).to(dtype)
+    x[:, :, ::3, 5] = torch.finfo(dtype).max
+    x[:, 1, ::7, 9] = -torch.finfo(dtype).max
+    c = Case(1, 2, L, fmt, block=block, empty=True)
+    cache, ws = c.upload(ad), ad.kv8_workspace()
+    ad.kv8_append(cache, x.cuda(), x.cuda(), 0, ws)
+    k, ks, v, vs, _ = c.download(cache)
+    for h in range(2):
+        want, sc = ref.append(np.zeros((L, D)), np.zeros(L // block), x[0, h].double().numpy(), 0, fmt, block)
+        assert np.array_equal(k[0, h], want) and np.array_equal(ks[0, h], sc)
+    kept = [*range(3, 20), *range(30, 63, 2)]
+    w = torch.zeros((1, 2, L), device="cuda")
+    w[..., kept] = 1.0
+    n = len(kept)
+    d = c if in_place else Case(1, 2, n, fmt, block=block, empty=True)
+    kw = {} if in_place else dict(dst=d.upload(ad))
+    ad.kv8_evict(cache, w, i32([L]), n, ws, **kw)
+    ad.check_workspace(ws)
+    got = d.download(kw.get("dst", cache))
+    for i, (st, sc) in ((0, (k, ks)), (2, (v, vs))):
+        for h in range(2):
+            vals = (st[0, h] * sc[0, h].repeat(block)[:, None])[kept]
+            assert np.abs(vals).max() == 2.0 ** 128
+            want, scale = ref.requantise(vals, fmt, block)
+            have = got[i][0, h, :n] * got[i + 1][0, h].repeat(block)[:n, None]
+            assert np.array_equal(have, want * scale.repeat(block)[:n, None]), (i, h)

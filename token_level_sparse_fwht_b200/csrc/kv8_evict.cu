@@ -390,7 +390,8 @@ __global__ void __launch_bounds__(kMoveThreads, kInPlace ? 1 : 2) kv8_move_kerne
         m2 = max_magnitude<FMT>(cur.w[u][j].w, m2);
       }
       const float m = __half2float(__hmax(__low2half(m2), __high2half(m2)));
-      uint32_t v = cur.s[u] != -1.0f ? __float_as_uint(finite_abs(m * cur.s[u])) + 1u : 0u;
+      // (256 x 2^120 stands for a value of up to fp32's largest that was rounded up)
+      uint32_t v = cur.s[u] != -1.0f ? __float_as_uint(fminf(m * cur.s[u], 0x1.fffffep127f)) + 1u : 0u;
       if (bs >= 8) {
         // the warp's eight rows lie in one block
         v = __reduce_max_sync(0xffffffffu, v);
