@@ -174,3 +174,33 @@ def test_evict_keeps_values_at_fp32s_largest(fmt, dtype, block, in_place):
             want, scale = ref.requantise(vals, fmt, block)
             have = got[i][0, h, :n] * got[i + 1][0, h].repeat(block)[:n, None]
             assert np.array_equal(have, want * scale.repeat(block)[:n, None]), (i, h)
+
+
+# --------------------------------------------------------------------------- binding
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float64])
+def test_calls_do_not_depend_on_torchs_default_type(dtype):
+    """A model's program often sets its own default type; what the calls make is float32 where it has to be."""
+    rng = np.random.default_rng(4)
+    x = torch.from_numpy(rng.standard_normal((2, 1, 2, 96, D))).to(torch.bfloat16).cuda()
+    q, w = torch.from_numpy(rng.standard_normal((1, 4, D))).float().cuda(), torch.rand((1, 2, 96), device="cuda")
+    idx = i32(rng.permuted(np.tile(np.arange(96), (1, 4, 1)), axis=-1)[..., :40].tolist())
+
+    def run():
+        cache, dst = (ad.kv8_cache(1, 2, n, block_size=16) for n in (96, 48))
+        ws = ad.kv8_attention_workspace(1, 4, 2, 96, weights=True)
+        ad.kv8_append(cache, x[0], x[1], 0, ws)
+        sums = w.clone()
+        outs = [ad.kv8_attention(q, cache, None, ws, weights=sums),
+                ad.kv8_sparse_attention(q, cache, idx, ad.kv8_sparse_attention_workspace(1, 4, 2, 40))]
+        keep, lens = ad.kv8_evict(cache, sums, i32([96]), 48, ws, sink=1, recent=5, dst=dst)
+        outs += [sums, keep, lens, *ad.kv8_read(dst, 0, 48, ws)]
+        ad.check_workspace(ws)
+        return outs
+
+    want, was = run(), torch.get_default_dtype()
+    torch.set_default_dtype(dtype)
+    try:
+        got = run()
+    finally:
+        torch.set_default_dtype(was)
+    assert all(torch.equal(a, b) and a.dtype == b.dtype for a, b in zip(got, want))

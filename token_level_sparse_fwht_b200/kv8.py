@@ -361,7 +361,8 @@ def kv8_evict(cache: KV8Cache, weights, seq_lens, budget: int, ws, sink: int = 0
         lens_out = seq_lens if lens_out is None else lens_out
     with _owner(cache.device, stream):
         if weights_out is None:
-            weights_out = torch.zeros((dst.B, dst.Hkv, dst.Lmax), device=cache.device)
+            weights_out = torch.zeros((dst.B, dst.Hkv, dst.Lmax), dtype=torch.float32,
+                                      device=cache.device)
         if lens_out is None:
             lens_out = torch.empty_like(seq_lens)
         if keep is None:
