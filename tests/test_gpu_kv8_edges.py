@@ -204,3 +204,26 @@ def test_calls_do_not_depend_on_torchs_default_type(dtype):
     finally:
         torch.set_default_dtype(was)
     assert all(torch.equal(a, b) and a.dtype == b.dtype for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("B,Hkv,n", [(2, 4, 1), (1, 4, 3), (3, 1, 5), (1, 1, 1)])
+def test_append_ignores_the_strides_of_dimensions_of_one_element(B, Hkv, n):
+    """One token a step: K a head-major tensor, V a slice of a token-major one, rows alike."""
+    rng = np.random.default_rng(B)
+    k = torch.from_numpy(rng.standard_normal((B, Hkv, n, D))).to(torch.bfloat16).cuda()
+    v = torch.empty((B, n, Hkv, D), dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+    if B == 1:                                        # one row of a batch laid out otherwise
+        v = torch.empty((2, Hkv, n, D), dtype=torch.bfloat16, device="cuda")[:1].as_strided(
+            (1, Hkv, n, D), (7, n * D, D, 1))
+    if Hkv == 1:
+        v = torch.empty((B, n, D), dtype=torch.bfloat16, device="cuda").as_strided(
+            (B, 1, n, D), (n * D, 24, D, 1))
+    v.copy_(-k)
+    a, b = (ad.kv8_cache(B, Hkv, 32, block_size=8, dtype=torch.int8) for _ in range(2))
+    ws = ad.kv8_workspace()
+    ad.kv8_append(a, k, v, 9, ws)
+    ad.kv8_append(b, k, (-k).contiguous(), 9, ws)
+    ad.check_workspace(ws)
+    for x, y in ((a.k, b.k), (a.v, b.v), (a.k_scale, b.k_scale), (a.v_scale, b.v_scale)):
+        assert torch.equal(x, y)
+    assert torch.equal(a.v, -a.k)

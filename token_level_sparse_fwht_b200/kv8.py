@@ -198,19 +198,20 @@ class PreparedKV8Append(_Call):
         B, Hkv, n, d = k_new.shape
         if (B, Hkv, d) != (cache.B, cache.Hkv, HEAD_DIM):
             raise ValueError("k_new must be [B, Hkv, n, 128] of the cache's B and Hkv")
-        if v_new.shape != k_new.shape or v_new.stride() != k_new.stride() or v_new.dtype != k_new.dtype:
+        # a dimension of one element may have any stride: it is never stepped
+        sb, sh, sn, sd = (0 if w == 1 else x for w, x in zip(k_new.shape, k_new.stride()))
+        v_strides = tuple(0 if w == 1 else x for w, x in zip(v_new.shape, v_new.stride()))
+        if v_new.shape != k_new.shape or v_strides != (sb, sh, sn, sd) or v_new.dtype != k_new.dtype:
             raise ValueError("v_new must have k_new's shape, strides and dtype")
         if not k_new.is_cuda or not v_new.is_cuda:
             raise ValueError("k_new and v_new must be CUDA tensors")
-        if k_new.stride(3) != 1:
+        if sd != 1:
             raise ValueError("rows of k_new must be contiguous")
         _same_device(cache.device, k_new=k_new, v_new=v_new, starts=starts, counts=counts)
         if cache.codes is not None and (t is None) == (ratio is None):
             raise ValueError("a cache with codes needs a threshold t or a ratio")
         if ratio is not None and not ratio > 0:
             raise ValueError("ratio must be in (0, 1]")
-        # a dimension of one element may have any stride: it is never stepped
-        sb, sh, sn = (0 if k_new.shape[i] == 1 else k_new.stride(i) for i in range(3))
         index, handle = _where(cache.device, stream)
         args = (cache.ptr, _c_p(k_new.data_ptr()), _c_p(v_new.data_ptr()), _c_i(_dtype_code(k_new)),
                 _c_i64(n), _c_i64(sb), _c_i64(sh), _c_i64(sn), _lens(cache, starts, "starts"),
