@@ -519,7 +519,7 @@ typedef struct {
 
 /*
  * Appends rows to an 8-bit cache.  Sequence b's counts[b] new rows (counts NULL: n_new
- * each; 0 <= counts[b] <= n_new) go to positions [starts[b], starts[b] + counts[b]);
+ * each; 0 <= counts[b] <= n_new, 1 <= n_new <= Lmax) go to positions [starts[b], starts[b] + counts[b]);
  * starts and counts are device int32 arrays [B].  k_new and v_new hold elements of
  * `dt`; row i of (b, h) starts at element b * stride_b + h * stride_h + i * stride_n
  * (the same strides for both, multiples of 16 bytes, >= 0), its d elements contiguous.

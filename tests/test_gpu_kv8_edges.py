@@ -227,3 +227,11 @@ def test_append_ignores_the_strides_of_dimensions_of_one_element(B, Hkv, n):
     for x, y in ((a.k, b.k), (a.v, b.v), (a.k_scale, b.k_scale), (a.v_scale, b.v_scale)):
         assert torch.equal(x, y)
     assert torch.equal(a.v, -a.k)
+
+
+@pytest.mark.parametrize("dtype,wide,first", [(torch.bfloat16, 132, 0), (torch.bfloat16, 136, 4),
+                                              (torch.float32, 130, 0), (torch.float32, 132, 2)])
+def test_append_names_rows_that_do_not_start_at_16_bytes(dtype, wide, first):
+    x = torch.zeros((1, 2, 3, wide), dtype=dtype, device="cuda")[..., first:first + D]
+    with pytest.raises(ValueError, match="16 bytes"):
+        ad.kv8_append(ad.kv8_cache(1, 2, 32, block_size=8), x, x, 0, ad.kv8_workspace())

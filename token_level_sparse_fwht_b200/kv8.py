@@ -207,6 +207,9 @@ class PreparedKV8Append(_Call):
             raise ValueError("k_new and v_new must be CUDA tensors")
         if sd != 1:
             raise ValueError("rows of k_new must be contiguous")
+        size = k_new.element_size()
+        if any(x * size % 16 for x in (sb, sh, sn)) or k_new.data_ptr() % 16 or v_new.data_ptr() % 16:
+            raise ValueError("rows of k_new and v_new must start at multiples of 16 bytes")
         _same_device(cache.device, k_new=k_new, v_new=v_new, starts=starts, counts=counts)
         if cache.codes is not None and (t is None) == (ratio is None):
             raise ValueError("a cache with codes needs a threshold t or a ratio")
@@ -230,10 +233,10 @@ def _starts(cache, starts, stream):
 
 def kv8_append(cache: KV8Cache, k_new, v_new, starts, ws, counts=None, t=None, ratio=None,
                stream=None):
-    """Quantises rows k_new, v_new [B,Hkv,n,128] (bf16 or float32, rows contiguous, other strides
-    free) into positions starts[b] .. of every sequence (starts: int32 [B], or one int for all);
-    counts [B] int32: how many of the n rows each sequence takes (default: all).  A cache
-    with codes gets the new keys' codes (threshold t, or ratio of each key's absmax)."""
+    """Quantises rows k_new, v_new [B,Hkv,n,128] (bf16 or float32, the same strides for both; rows
+    contiguous, each starting at a multiple of 16 bytes) into positions starts[b] .. of every
+    sequence (starts: int32 [B], or one int for all); counts [B] int32: how many of the n rows
+    (n at most the cache's Lmax) each sequence takes (default: all).  A cache with codes gets the new keys' codes (threshold t, or ratio of each key's absmax)."""
     PreparedKV8Append(cache, k_new, v_new, _starts(cache, starts, stream), ws, counts, t, ratio,
                       stream)()
     return cache
