@@ -627,7 +627,8 @@ adamas_status adamas_compact_rows(const void* src, void* dst, int row_bytes, int
  * positions 0 .. n - 1 of `dst` (K, V, and codes when dst->codes is given), requantised
  * block by block: S(largest magnitude of the block's kept values), bytes rounded from
  * the kept values.  A block in place whose rows all stay where they are keeps bytes and
- * scale.  lens_out[b] = min(seq_lens[b], budget) (lens_out may equal seq_lens).  dst may be
+ * scale.  lens_out[b] = min(seq_lens[b], budget) (lens_out may equal seq_lens, and not
+ * overlap it otherwise).  dst may be
  * the same cache (in place) or one that shares no memory with src, of the same format,
  * B and Hkv, with dst->Lmax >= budget.  weights_out is [B][Hkv][dst->Lmax].  Rows behind
  * the kept ones keep their bytes, but those of the last kept row's block not their scale; so does

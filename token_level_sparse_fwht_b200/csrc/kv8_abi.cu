@@ -318,6 +318,9 @@ adamas_status adamas_kv8_evict(const adamas_kv8_cache* src, const adamas_kv8_cac
   s = check_cache(dst, b);
   if (s != ADAMAS_OK) return s;
   if (!weights_out || !lens_out || !aligned(lens_out, 4)) return ADAMAS_ERR_INVALID_ARG;
+  const size_t len_bytes = size_t(a.B) * 4;
+  if (lens_out != seq_lens && overlap({seq_lens, len_bytes}, {lens_out, len_bytes}))
+    return ADAMAS_ERR_INVALID_ARG;
   if (src->format != dst->format || a.B != b.B || a.Hkv != b.Hkv || b.Lmax < budget)
     return ADAMAS_ERR_INVALID_ARG;
   if (b.codes && !a.codes) return ADAMAS_ERR_INVALID_ARG;
