@@ -600,7 +600,8 @@ adamas_status adamas_kv8_sparse_attention(const void* q, adamas_dtype dt,
  * keep [B][Hkv][budget] int32 receives them ascending, then -1.  weights_out (nullable,
  * [B][Hkv][Lmax_out], Lmax_out >= budget; may equal weights when Lmax_out = Lmax)
  * receives the kept weights at 0 .. n - 1 and zeros at n .. min(seq_lens[b], Lmax_out) - 1.
- * Lmax at most 786432 (ADAMAS_ERR_UNSUPPORTED above).
+ * Lmax at most 786432, and 393216 on a device that has no room for a cluster of 16 CTAs
+ * (ADAMAS_ERR_UNSUPPORTED above).
  */
 adamas_status adamas_evict_select(const float* weights, int B, int Hkv, int64_t Lmax,
                                   const int32_t* seq_lens, int budget, int sink, int recent,

@@ -235,3 +235,46 @@ def test_append_names_rows_that_do_not_start_at_16_bytes(dtype, wide, first):
     x = torch.zeros((1, 2, 3, wide), dtype=dtype, device="cuda")[..., first:first + D]
     with pytest.raises(ValueError, match="16 bytes"):
         ad.kv8_append(ad.kv8_cache(1, 2, 32, block_size=8), x, x, 0, ad.kv8_workspace())
+
+
+# ------------------------------------------------------------------- the longest selections
+@pytest.mark.parametrize("B,L,budget,sink,recent", [(1, 393216, 1000, 0, 0), (1, 393217, 200000, 7, 1000),
+                                                    (2, 600001, 50001, 0, 64), (1, 786432, 300000, 4, 5000),
+                                                    (1, 786432, 786431, 0, 0), (1, 786432, 17, 3, 14)])
+def test_evict_select_of_the_longest_sequences(B, L, budget, sink, recent):
+    """Clusters of 8 and of 16 CTAs; a tie over about a third of the positions crosses every share."""
+    rng = np.random.default_rng(budget)
+    w = rng.random((B, 1, L)).astype(np.float32)
+    w[rng.random((B, 1, L)) < 1 / 3] = 0.75
+    w[..., rng.integers(0, L, 50)] = np.nan
+    lens = [L, L - 77777][:B]
+    ws, out = ad.kv8_workspace(), torch.from_numpy(w).cuda()
+    keep = ad.evict_select(out, i32(lens), budget, ws, sink=sink, recent=recent, weights_out=out)
+    ad.check_workspace(ws)
+    keep, out = keep.cpu().numpy(), out.cpu().numpy()
+    for b in range(B):
+        want = ref.evict_select(w[b, 0], lens[b], budget, sink, recent)
+        n = len(want)
+        assert np.array_equal(keep[b, 0, :n], want) and (keep[b, 0, n:] == -1).all()
+        assert np.array_equal(out[b, 0, :n], w[b, 0, want], equal_nan=True)
+        assert (out[b, 0, n:lens[b]] == 0).all()
+        assert np.array_equal(out[b, 0, lens[b]:], w[b, 0, lens[b]:], equal_nan=True)
+
+
+def test_evict_of_a_long_cache():
+    """Selection by 16 CTAs, then the move in place, against the definition."""
+    L, budget = 400000, 9000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    cache = ad.kv8_cache(1, 1, L, block_size=64)
+    x = torch.randn((1, 1, L, D), generator=g, device="cuda", dtype=torch.float32)
+    ws = ad.kv8_workspace()
+    ad.kv8_append(cache, x, -x, 0, ws)
+    k, v = ad.kv8_read(cache, 0, L, ws, dtype=torch.float32)
+    w = torch.rand((1, 1, cache.Lmax), generator=g, device="cuda")
+    want = ref.evict_select(w[0, 0].cpu().numpy(), L, budget, 4, 256)
+    keep, lens = ad.kv8_evict(cache, w, i32([L]), budget, ws, sink=4, recent=256)
+    ad.check_workspace(ws)
+    assert np.array_equal(keep[0, 0].cpu().numpy(), want) and lens.tolist() == [budget]
+    for got, old in zip(ad.kv8_read(cache, 0, budget, ws, dtype=torch.float32), (k, v)):
+        stored, scale = ref.requantise(old[0, 0, keep[0, 0].long()].double().cpu().numpy(), "e4m3", 64)
+        assert np.array_equal(got[0, 0].double().cpu().numpy(), stored * scale.repeat(64)[:budget, None])

@@ -583,6 +583,15 @@ cudaError_t launch_evict_select(const float* w, int B, int Hkv, int64_t Lmax,
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = sizeof(SelSmem) + size_t(share) * 4 + size_t(share) / 4;
   cfg.stream = stream;
+  if (cs > 8) {
+    // above the portable size whether 16 such CTAs find room in one GPC is the device's affair
+    int fit = 0;
+    cfg.numAttrs = 1;   // the cluster's shape alone
+    const cudaError_t q = cudaOccupancyMaxActiveClusters(&fit, evict_select_kernel, &cfg);
+    if (q != cudaSuccess) return q;
+    if (fit < 1) return cudaErrorNotSupported;
+    cfg.numAttrs = 2;
+  }
   return cudaLaunchKernelEx(&cfg, evict_select_kernel, w, Hkv, Lmax, seq_lens, budget, sink,
                             recent, keep, w_out, Lmax_out, cs, share, err);
 }
