@@ -555,6 +555,12 @@ adamas_status adamas_kv8_read(const adamas_kv8_cache* cache, const int32_t* star
  * int32 [B], each in [0, Lmax] (others are clamped and recorded); NULL: Lmax each.  A
  * sequence of length 0 gives zeros.  Any G = Hq / Hkv from 1 to 8.
  *
+ * Precision.  Scores, softmax statistics and sums are fp32.  The products take q and
+ * p_j S_v(j) (softmax weight times the scale of V's block) in two fp16 parts: an element of
+ * q is held to 2^-22 of itself or 2^-39 of its head's largest, p_j S_v(j) to 2^-22 of
+ * itself or 2^-37 of its head's largest, whichever is more.  A dimension in which the
+ * blocks of the largest p S_v hold zeros thus keeps 37 - r bits of blocks 2^r smaller.
+ *
  * With weights_out (device float32 [B][Hkv][Lmax]) every position's attention weight,
  * summed over the G query heads of its kv head, is added to weights_in:
  * weights_out[b][kv][j] = weights_in[b][kv][j] + sum_g p_g(j) for j < seq_lens[b]; other

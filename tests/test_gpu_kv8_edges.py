@@ -87,6 +87,65 @@ def test_many_keys_of_very_small_values(fmt, e, L, block):
     check(out, want, tol, "out")
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("block", [4, 16])
+@pytest.mark.parametrize("r", [0, 8, 16, 20, 24, 28])
+def test_small_blocks_show_where_large_ones_hold_zeros(fmt, dtype, block, r):
+    """p c is held in two fp16 parts under one reference per head: to 2^-22 of itself or 2^-37 of the
+    head's largest (w > 2^12 at least there, and the second part's half step is 2^-25).  Half of
+    the blocks have 2^r times the scale of the others and zeros in the upper dimensions, where the others
+    hold positive values; there the bound is 2^(r - 37) of the output and what the sums drop."""
+    L = 256
+    c = Case(1, 1, L, fmt, block=block, seed=r, spread=0)
+    c.ks[:] = 2.0 ** -6
+    large = np.arange(L) // block % 2 == 0
+    c.v[:, :, large, D // 2:] = 0
+    c.v[:, :, ~large, D // 2:] = ref.round8(np.abs(c.v[:, :, ~large, D // 2:]) + 1, fmt)
+    c.vs[:] = np.where(large[::block], 2.0 ** r, 1.0)
+    q = torch.randn((1, 4, D), generator=torch.Generator().manual_seed(r)).to(dtype)
+    want, tol, _, _ = attention_oracle(q.double().numpy(), c, lambda b, h: np.arange(L))
+    # the bound (2^-9 of the largest p at r = 28, a few times the mean) is far under what is compared: a
+    # block lost would show
+    assert (tol[..., D // 2:] < 2.0 ** -6 * want[..., D // 2:]).all()
+    cache = c.upload(ad)
+    ws = ad.kv8_attention_workspace(1, 4, 1, L)
+    out = ad.kv8_attention(q.cuda(), cache, i32([L]), ws)
+    check(out, want, tol, "dense")
+    sws = ad.kv8_sparse_attention_workspace(1, 4, 1, L)
+    idx = np.random.default_rng(r).permuted(np.tile(np.arange(L), (1, 4, 1)), axis=-1)
+    check(ad.kv8_sparse_attention(q.cuda(), cache, i32(idx.tolist()), sws), want, tol, "sparse")
+    ad.check_workspace(ws)
+    ad.check_workspace(sws)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("r", [0, 8, 14, 18])
+def test_small_query_elements_show_where_keys_hold_zeros(fmt, dtype, r):
+    """One element of q is 2^r times the others and meets zeros: scores come from the others alone, which
+    are held to 2^-22 of themselves (in the helper's bound) or 2^-39 of the largest, in
+    every product: |dx| <= 2^-39 max|q| a sum|k| / sqrt(d), and an output's change e^(2 dx) of
+    its terms."""
+    L = 200
+    c = Case(1, 1, L, fmt, block=8, seed=r, spread=0)
+    c.k[..., 3] = 0
+    c.ks[:] = 2.0 ** -5
+    q = torch.randn((1, 4, D), generator=torch.Generator().manual_seed(r))
+    q[..., 3] = 2.0 ** r * 4
+    q = q.to(dtype)
+    want, tol, ww, wtol = attention_oracle(q.double().numpy(), c, lambda b, h: np.arange(L))
+    K, V = c.values()
+    dx = 2.0 ** -39 * q.abs().double().max().item() * np.abs(K[0, 0, :L]).sum(-1).max() / np.sqrt(D)
+    assert dx < 2.0 ** -10
+    tol = tol + 2.1 * dx * np.abs(V[0, 0, :L]).max(0)
+    ws, w = ad.kv8_attention_workspace(1, 4, 1, c.cap, weights=True), torch.zeros((1, 1, c.cap), device="cuda")
+    out = ad.kv8_attention(q.cuda(), c.upload(ad), i32([L]), ws, weights=w)
+    ad.check_workspace(ws)
+    check(out, want, tol, "out")
+    check(w, ww, wtol + 2.1 * dx * ww + 2.0 ** -140, "weights")
+
+
 # ----------------------------------------------------------------- eviction: bad pages
 # Positions 32 .. 47 of sequence 0 are on a page that does not exist.  Kept lists whose rows from there
 # are the first of a block, in its middle and its end, several blocks, and a whole block.

@@ -13,9 +13,14 @@
 //
 // The work is 256 bytes of cache per key against 4 G d operations: HBM bounds it.  The
 // tensor cores (mma.m16n8k16, fp16 operands, fp32 sums) keep the arithmetic out of the
-// way; a byte of either format is exact in fp16.  Precision stays that of fp32: q is split
-// into two fp16 parts (fp32 queries; a bf16 value is exact in one), scaled by a power of
-// two per head, and so is w_j (times 2^14), each sum taking both parts.
+// way; a byte of either format is exact in fp16.  q and w_j are split into two fp16 parts (a bf16
+// q takes one), scaled by powers of two so that a head's largest |q| lies in [2^14, 2^15) and its
+// largest w in (2^12, 2^14]; each sum takes both parts.  The parts hold 2^-22 of a value, and
+// never less than fp16's half step 2^-25: an element of q is off by at most 2^-22 of itself
+// or 2^-39 of its head's largest, a product p_j c_j by 2^-22 of itself or 2^-37 of its
+// head's largest.  So what a block adds to a dimension loses bits where another block's p c is
+// 2^15 and more times larger, and shows only if that block holds zeros there.  Three parts,
+// or bf16 ones (no conversion from e4m3), would cost registers that the loop does not have.
 //   scores: A = q (16 rows: 8 head rows, high parts; 8 rows of low parts), B = K^T.
 //   values: A = V^T (16 dimensions x 16 keys), B = w^T (16 keys x 8 columns).
 // The score fragment a lane gets (its head row, keys 2q, 2q+1 of two 8-key tiles) is the
