@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import token_level_sparse_fwht_b200 as ad
 from kv8_helpers import D, Case, attention_oracle, check
 from oracle import kv8_ref as ref
@@ -337,3 +338,45 @@ def test_evict_of_a_long_cache():
     for got, old in zip(ad.kv8_read(cache, 0, budget, ws, dtype=torch.float32), (k, v)):
         stored, scale = ref.requantise(old[0, 0, keep[0, 0].long()].double().cpu().numpy(), "e4m3", 64)
         assert np.array_equal(got[0, 0].double().cpu().numpy(), stored * scale.repeat(64)[:budget, None])
+
+
+# ------------------------------------------------------------------------- codes of append
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("block", [1, 8, 16, 64, 256])
+@pytest.mark.parametrize("kw", [dict(t=1.01), dict(ratio=0.5)])
+def test_append_codes_of_every_form(dtype, fmt, block, kw):
+    """Rows from inside a block on, over several blocks: the codes are the definition's and the encoder's but
+    for coordinates next to a threshold (fp32 sums of 128: within 1e-4 of the vector's scale, as for
+    the encoder), other positions keep theirs."""
+    B, Hkv, L, n = 2, 2, 512, 300
+    starts, counts = [5, 201], [n, 77]
+    c = Case(B, Hkv, L, fmt, block=block, seed=block, codes=True)
+    c.codes[:] = np.random.default_rng(1).integers(0, 256, c.codes.shape, dtype=np.uint8)
+    x = torch.from_numpy(np.random.default_rng(block + 1).standard_normal((B, Hkv, n, D)) * 1.3).to(dtype)
+    x[:, :, ::5] *= 8
+    cache, ws = c.upload(ad), ad.kv8_workspace()
+    ad.kv8_append(cache, x.cuda(), x.cuda(), i32(starts), ws, counts=i32(counts), **kw)
+    ad.check_workspace(ws)
+    codes = c.download(cache)[4]
+    enc = torch.zeros((B, Hkv, n, 32), dtype=torch.uint8, device="cuda")
+    if "t" in kw:
+        ad.encode_keys(x.cuda(), enc, 0, n, kw["t"])
+    else:
+        ad.encode_keys_absmax(x.cuda(), enc, 0, n, kw["ratio"])
+    for b in range(B):
+        rows = x[b, :, :counts[b]].double().numpy()
+        y = oracle.hadamard_rotate(rows)
+        if "t" in kw:
+            want, margin = oracle.bucketize(y, kw["t"]), oracle.threshold_margin(y, kw["t"])
+        else:
+            t = oracle.absmax_thresholds(rows, kw["ratio"])
+            want = oracle.bucketize_per_vector(y, t)
+            margin = np.minimum(np.abs(np.abs(y) - np.asarray(t).reshape(*y.shape[:-1], 1)), np.abs(y))
+        near = margin < 1e-4 * np.maximum(1.0, np.abs(y).max(-1, keepdims=True))
+        got = oracle.unpack_codes(codes[b, :, starts[b]:starts[b] + counts[b]])
+        theirs = oracle.unpack_codes(enc[b, :, :counts[b]].cpu().numpy())
+        assert not ((got != want) & ~near).any() and not ((got != theirs) & ~near).any()
+        rest = np.ones(c.cap, bool)
+        rest[starts[b]:starts[b] + counts[b]] = False
+        assert np.array_equal(codes[b][:, rest], c.codes[b][:, rest])
