@@ -797,21 +797,23 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
         for (int i = 0; i < kSc; ++i) sf[u][i] = ksc[u][i] * factor;
       }
       load_k(r1);
-      // ---- references.  The value scale's exponent is rounded up.
-      float up = -INFINITY, up2 = -INFINITY;
+      // ---- references.  ve: the value scale's exponent plus 1, so that c < 2^ve.
+      float up = -INFINITY, up2 = -INFINITY, ve[2][kSc];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         float half = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kSc; ++i) ve[u][i] = float(int(__float_as_uint(vsc[u][i]) >> 23) - 126);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float y = there(u, i) ? x[u][i] * sf[u][kUni ? 0 : i] : -INFINITY;
           half = fmaxf(half, y);
           if (!kUni)
-            up2 = fmaxf(up2, y + float(int(__float_as_uint(vsc[u][kUni ? 0 : i]) >> 23) - 126));
+            up2 = fmaxf(up2, y + ve[u][kUni ? 0 : i]);
         }
         up = fmaxf(up, half);
         if (kUni)
-          up2 = fmaxf(up2, half + float(int(__float_as_uint(vsc[u][0]) >> 23) - 126));
+          up2 = fmaxf(up2, half + ve[u][0]);
       }
       if (a.scores != nullptr && (NT == 2 || gid < 4) && head_ok) {
         float* const o = a.scores + (unit * a.G + head) * a.score_stride + cur.ls * kStep +
@@ -845,18 +847,20 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
         m = mn;
         m2 = m2n;
       }
-      // w = 2^(x + E - m2 + 14) (c / 2^E), E the exponent of c: formed by itself, since p and
-      // 2^(m - m2) c can each leave the range of fp32 where w does not (a block of zeros may lead by 100
-      // and more, and m2 then lies as far below m).  E is held to 126 so that 2^-E is normal.
+      // w = 2^(x + E - m2 + 14) (c / 2^E), E = ve - 1: formed by itself, since p and 2^(m - m2) c can
+      // each leave the range of fp32 where w does not (a block of zeros may lead by 100 and more,
+      // and m2 then lies as far below m).  c / 2^E is c's mantissa, but for scales below 2^-126 (and 0).
+      const float ref_w = (kWBias - 1.0f) - m2;
       uint32_t b[2][NT][2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         float up_w[kSc], mant[kSc];
 #pragma unroll
         for (int i = 0; i < kSc; ++i) {
-          const int e = min(max(int(__float_as_uint(vsc[u][i]) >> 23) - 127, -126), 126);
-          up_w[i] = (float(e) + kWBias) - m2;
-          mant[i] = vsc[u][i] * pow2i(-e);
+          const uint32_t bits = __float_as_uint(vsc[u][i]);
+          up_w[i] = ve[u][i] + ref_w;
+          mant[i] = bits < 0x800000u ? vsc[u][i] * 0x1p127f
+                                     : __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
         }
         float w[4];
 #pragma unroll
