@@ -147,6 +147,55 @@ def test_small_query_elements_show_where_keys_hold_zeros(fmt, dtype, r):
     check(w, ww, wtol + 2.1 * dx * ww + 2.0 ** -140, "weights")
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("block", [8, 32])
+@pytest.mark.parametrize("e", [0, 10, 14, 16, 18, 20, 24, 40, 90])
+@pytest.mark.parametrize("G", [2, 5])
+def test_scores_of_any_size_choose_the_leading_keys(fmt, dtype, block, e, G):
+    """Scores of about 2^10 2^e.  Every head has three keys that lead all others by more than the scores'
+    rounding (20 units of 2^-23 of sum |q k|, and 40 for the exponential): copies of the head's
+    query, one of them stored with half its bytes' size under twice the scale, so all products are
+    equal.  The output is the mean of their three values, to the exponential's and the sums' last bits."""
+    L = 700
+    c = Case(1, 1, L, fmt, block=block, seed=e, spread=0)
+    q = torch.randn((1, G, D), generator=torch.Generator().manual_seed(e)).to(dtype)
+    c.ks[:] = 2.0 ** e
+    lead = np.random.default_rng(e).permutation(c.cap // block - 2)[:3 * G].reshape(G, 3) * block + 1
+    for h in range(G):
+        x = q[0, h].double().numpy()
+        row = ref.round8(x / np.abs(x).max() * ref.FMAX[fmt] / 4, fmt) * 2
+        for n, p in enumerate(lead[h]):
+            c.k[0, 0, p] = row / 2 if n == 1 else row
+            if n == 1:
+                c.ks[0, 0, p // block] = 2.0 ** (e + 1)
+                c.k[0, 0, p + 1:p // block * block + block] /= 2
+                c.k[0, 0, p // block * block:p] /= 2
+                c.k[0, 0, p // block * block:][:block] = ref.round8(c.k[0, 0, p // block * block:][:block], fmt)
+    K, V = (x[0, 0, :L] for x in c.values())
+    want, others, S = np.zeros((1, G, D)), np.ones((G, L), bool), 0.0
+    for h in range(G):
+        x = K @ q[0, h].double().numpy() / np.sqrt(D)
+        others[h, lead[h]] = False
+        S = (np.abs(K) @ np.abs(q[0, h].double().numpy())).max() / np.sqrt(D)
+        assert np.ptp(x[lead[h]]) == 0 and x[lead[h][0]] - x[others[h]].max() > 20 * 2.0 ** -23 * S + 40
+        want[0, h] = V[lead[h]].mean(0)
+    tol = np.broadcast_to(2.0 ** -20 * np.abs(V).max(), want.shape)
+    cache, lens = c.upload(ad), i32([L])
+    ws = ad.kv8_attention_workspace(1, G, 1, c.cap, weights=True)
+    w = torch.zeros((1, 1, c.cap), device="cuda")
+    check(ad.kv8_attention(q.cuda(), cache, lens, ws, weights=w), want, tol, "dense")
+    ww = np.zeros((1, 1, c.cap))
+    np.add.at(ww[0, 0], lead.ravel(), 1 / 3)
+    check(w, ww, np.full_like(ww, 2.0 ** -20), "weights")
+    sws, w = ad.kv8_sparse_attention_workspace(1, G, 1, L, weights=True), torch.zeros_like(w)
+    idx = np.random.default_rng(1).permuted(np.tile(np.arange(L), (1, G, 1)), axis=-1)
+    check(ad.kv8_sparse_attention(q.cuda(), cache, i32(idx.tolist()), sws, weights=w), want, tol, "sparse")
+    check(w, ww, np.full_like(ww, 2.0 ** -20), "sparse weights")
+    ad.check_workspace(ws)
+    ad.check_workspace(sws)
+
+
 # ----------------------------------------------------------------- eviction: bad pages
 # Positions 32 .. 47 of sequence 0 are on a page that does not exist.  Kept lists whose rows from there
 # are the first of a block, in its middle and its end, several blocks, and a whole block.

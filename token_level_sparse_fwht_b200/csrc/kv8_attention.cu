@@ -7,9 +7,10 @@
 //   x_j = (q . k_j) a_j log2(e) / sqrt(d),  out = sum_j 2^(x_j - M) c_j v_j / sum_j 2^(x_j - M).
 // One pass over the keys with running references instead of maxima: m is an INTEGER at or
 // above every x_j seen (so 2^(x - m) is formed by one fused multiply-add and every change
-// of reference, in a warp or between partial results, is an exact power of two), and
-// m2 bounds x_j + log2 c_j the same way for the value sum, whose terms
-// w_j = 2^(x_j - m2) c_j then lie in [0, 1] whatever the scales are.
+// of reference, in a warp or between partial results, is an exact power of two), and the
+// integer r bounds x_j - m + log2 c_j the same way for the value sum, whose terms
+// w_j = 2^(x_j - m - r) c_j then lie in [0, 1] whatever the scales are.  r is relative to m, since a
+// sum m + r of a large m would lose r's last bits.
 //
 // The work is 256 bytes of cache per key against 4 G d operations: HBM bounds it.  The
 // tensor cores (mma.m16n8k16, fp16 operands, fp32 sums) keep the arithmetic out of the
@@ -70,14 +71,14 @@ constexpr int kStages = 3;                       // tiles of a warp's ring (gath
 constexpr int kStage = 2 * kTile * kD;            // bytes: K rows, then V rows
 constexpr int kMaxParts = 512;                   // CTAs, and so parts of a unit
 constexpr float kWBias = 14.0f;                  // w is held times 2^14
-constexpr int kPart = 4 + kD;                    // floats of a partial: m, l, m2, 0, sums
+constexpr int kPart = 4 + kD;                    // floats of a partial: m, l, r, 0, sums
 
 // Shared memory of a CTA.
 template <int NT>
 struct Smem {
   static constexpr int kSums = NT == 1 ? 16 : 32;   // values per lane when warps are merged
   float sums[kWarps][kSums][32];                    // merge of the warps
-  float stat[kWarps][8][4];                         // m, l, m2 per warp and head
+  float stat[kWarps][8][4];                         // m, l, r per warp and head
 };
 
 struct Args {
@@ -131,13 +132,23 @@ __device__ __forceinline__ float ref_change(float from, float to) {
   return from == to ? 1.0f : ex2(from - to);
 }
 
-// What turns a head's value sum t into its output t 2^(m2 - m - 14) / l, in two factors: with small
-// value scales m2 lies up to 126 below m, and the whole factor below fp32's normal numbers although
-// t times it may not.  The second is 1 but for exponents below -100.
+// How far reference m lies below the common one M >= m (0 if equal, also where both are -inf).
+__device__ __forceinline__ float ref_step(float m, float M) { return m == M ? 0.0f : m - M; }
+
+// The references (m, r) of two sets of terms become those of both: r is relative to m.
+__device__ __forceinline__ void ref_join(float& m, float& r, float m1, float r1) {
+  const float top = fmaxf(m, m1);
+  r = fmaxf(r + ref_step(m, top), r1 + ref_step(m1, top));
+  m = top;
+}
+
+// What turns a head's value sum t into its output t 2^(r - 14) / l, in two factors: with small value
+// scales r is as low as -126, and the whole factor below fp32's normal numbers although t times
+// it may not.  The second is 1 but for exponents below -100.
 struct OutScale {
   float f, g;
-  __device__ __forceinline__ OutScale(float m, float m2, float l, bool some) {
-    const float e = m2 - m - kWBias, e1 = fmaxf(e, -100.0f);
+  __device__ __forceinline__ OutScale(float r, float l, bool some) {
+    const float e = r - kWBias, e1 = fmaxf(e, -100.0f);
     f = some ? ex2(e1) / l : 0.0f;
     g = some ? ex2(e - e1) : 0.0f;
   }
@@ -368,15 +379,16 @@ __host__ __device__ inline int whole_units(int units, int steps_per_unit, int gr
 // unit of at most kFewParts parts is merged by the block of its first CTA, a warp per head; of one in more
 // (so cut into at least a first, 7 inner and a last part) the block of part h takes head h, thread p
 // finding part p's factor before warp w sums parts w, w + 8, ..., 4 dimensions per lane.  So one
-// long sequence among many short ones is not left to a warp.  (With blocks for all heads of every CTA
+// long sequence among many short ones is not left to a warp.  (The launch bound of 2 blocks is for the
+// 80 registers that hold a warp's 8 parts at once; left to itself the compiler took 64, and two rounds.)  (With blocks for all heads of every CTA
 // one sequence of 1000 keys took 8.4 us and one of 32K 19.6, so 7.9 and 19.4.)
 constexpr int kCombineThreads = 256, kFewParts = 8;
 
-__global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(
+__global__ void __launch_bounds__(kCombineThreads, 2) kv8_combine_kernel(
     const int4* __restrict__ cuts, const float* __restrict__ part, int G, float* __restrict__ stats,
     float* __restrict__ out) {
   constexpr int kBatch = 10, kW = kCombineThreads / 32;
-  __shared__ float fac[kMaxParts];
+  __shared__ float ref[kMaxParts];
   __shared__ float red[3][kW];
   __shared__ float4 sums[kW][32];
   pdl_wait();
@@ -388,10 +400,10 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(
   if (parts < 2 || (by_warp ? cut.w != 0 || warp >= G : cut.w >= G)) return;
   const int h = by_warp ? warp : cut.w, c = blockIdx.x - cut.w;
   const int64_t unit = (int64_t(uint32_t(cut.y)) << 32) | uint32_t(cut.x);
-  const auto finish = [&](float l, float M, float M2, const float4& t) {
+  const auto finish = [&](float l, float M, float R, const float4& t) {
     const bool some = l > 0.0f || !(l == l);   // an empty list: zeros
     reinterpret_cast<float4*>(out + (unit * G + h) * kD)[lane] =
-        OutScale(M, M2, l, some).of(t.x, t.y, t.z, t.w);
+        OutScale(R, l, some).of(t.x, t.y, t.z, t.w);
     if (stats != nullptr && lane == 0) {
       float* const o = stats + (unit * G + h) * 2;
       o[0] = some ? M : 0.0f;
@@ -411,23 +423,23 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(
       w[p] = ok ? __ldcg(at(p)) : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
       y[p] = ok ? __ldcg(at(p) + 1 + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    float M = -INFINITY, M2 = -INFINITY, l = 0.0f;
+    float M = -INFINITY, R = -INFINITY, l = 0.0f;
 #pragma unroll
-    for (int p = 0; p < kFewParts; ++p) {
-      M = fmaxf(M, w[p].x);
-      M2 = fmaxf(M2, w[p].z);
-    }
+    for (int p = 0; p < kFewParts; ++p) M = fmaxf(M, w[p].x);
+#pragma unroll
+    for (int p = 0; p < kFewParts; ++p) R = fmaxf(R, w[p].z + ref_step(w[p].x, M));
     float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int p = 0; p < kFewParts; ++p) {
-      l += w[p].y * ref_change(w[p].x, M);
-      const float f = ref_change(w[p].z, M2);
+      const float step = ref_step(w[p].x, M);
+      l += w[p].y * ex2(step);
+      const float f = ref_change(w[p].z + step, R);
       t.x = fmaf(y[p].x, f, t.x);
       t.y = fmaf(y[p].y, f, t.y);
       t.z = fmaf(y[p].z, f, t.z);
       t.w = fmaf(y[p].w, f, t.w);
     }
-    finish(l, M, M2, t);
+    finish(l, M, R, t);
     return;
   }
   float4 y[kBatch];
@@ -440,41 +452,41 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(
     }
   };
   load(warp);   // under way while the factors are found
-  float M = -INFINITY, M2 = -INFINITY;
-  float4 st[(kMaxParts + kCombineThreads - 1) / kCombineThreads];
+  constexpr int kSt = (kMaxParts + kCombineThreads - 1) / kCombineThreads;
+  float M = -INFINITY, R = -INFINITY;
+  float4 st[kSt];
 #pragma unroll
-  for (int i = 0; i < int(sizeof(st) / sizeof(st[0])); ++i) {
+  for (int i = 0; i < kSt; ++i) {
     const int p = tid + i * kCombineThreads;
     st[i] = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
     if (p < parts) st[i] = __ldcg(at(p));
     M = fmaxf(M, st[i].x);
-    M2 = fmaxf(M2, st[i].z);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    M2 = fmaxf(M2, __shfl_xor_sync(0xffffffffu, M2, o));
-  }
-  if (lane == 0) {
-    red[0][warp] = M;
-    red[1][warp] = M2;
-  }
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) red[0][warp] = M;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kW; ++w) {
-    M = fmaxf(M, red[0][w]);
-    M2 = fmaxf(M2, red[1][w]);
-  }
+  for (int w = 0; w < kW; ++w) M = fmaxf(M, red[0][w]);
   float l = 0.0f;
 #pragma unroll
-  for (int i = 0; i < int(sizeof(st) / sizeof(st[0])); ++i) {
+  for (int i = 0; i < kSt; ++i) {
     const int p = tid + i * kCombineThreads;
-    l += st[i].y * ref_change(st[i].x, M);
-    if (p < parts) fac[p] = ref_change(st[i].z, M2);
+    const float step = ref_step(st[i].x, M), r = st[i].z + step;
+    l += st[i].y * ex2(step);
+    R = fmaxf(R, r);
+    if (p < parts) ref[p] = r;
   }
   l = warp_sum(l);
-  if (lane == 0) red[2][warp] = l;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) R = fmaxf(R, __shfl_xor_sync(0xffffffffu, R, o));
+  if (lane == 0) {
+    red[1][warp] = R;
+    red[2][warp] = l;
+  }
   __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kW; ++w) R = fmaxf(R, red[1][w]);
   float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int p0 = warp; p0 < parts; p0 += kBatch * kW) {
     if (p0 != warp) load(p0);
@@ -482,7 +494,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(
     for (int u = 0; u < kBatch; ++u) {
       const int p = p0 + u * kW;
       if (p < parts) {
-        const float f = fac[p];
+        const float f = ref_change(ref[p], R);
         t.x = fmaf(y[u].x, f, t.x);
         t.y = fmaf(y[u].y, f, t.y);
         t.z = fmaf(y[u].z, f, t.z);
@@ -504,7 +516,7 @@ __global__ void __launch_bounds__(kCombineThreads) kv8_combine_kernel(
     t.z += x.z;
     t.w += x.w;
   }
-  finish(l, M, M2, t);
+  finish(l, M, R, t);
 }
 
 // FMT: byte format; NT: value products per 16 keys (1: G <= 4, 2: G <= 8).
@@ -727,7 +739,8 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
 
   uint32_t qh[8][2], ql[kLo ? 8 : 1][2];
   float factor = 0.0f;
-  float m = -INFINITY, m2 = -INFINITY, l = 0.0f;
+  float m = -INFINITY, r = -INFINITY, l = 0.0f;
+  bool big = false;   // this lane's m is at least 256 in magnitude
   float acc[8][4];
   bool fresh = true;
   int4 cut_here = make_int4(0, 0, 0, 0);   // the unit that ends in a later CTA
@@ -735,7 +748,8 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
     const int64_t unit = int64_t(cur.b) * a.U + cur.j;
     if (fresh) {
       factor = query_fragments<T, kLo>(qrow, a.scale_log2, qh, ql);
-      m = m2 = -INFINITY;
+      m = r = -INFINITY;
+      big = false;
       l = 0.0f;
 #pragma unroll
       for (int t = 0; t < 8; ++t)
@@ -799,6 +813,9 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
       load_k(r1);
       // ---- references.  ve: the value scale's exponent plus 1, so that c < 2^ve.
       float up = -INFINITY, up2 = -INFINITY, ve[2][kSc];
+      const auto y = [&](int u, int i) {
+        return there(u, i) ? x[u][i] * sf[u][kUni ? 0 : i] : -INFINITY;
+      };
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         float half = -INFINITY;
@@ -806,37 +823,56 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
         for (int i = 0; i < kSc; ++i) ve[u][i] = float(int(__float_as_uint(vsc[u][i]) >> 23) - 126);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float y = there(u, i) ? x[u][i] * sf[u][kUni ? 0 : i] : -INFINITY;
-          half = fmaxf(half, y);
-          if (!kUni)
-            up2 = fmaxf(up2, y + ve[u][kUni ? 0 : i]);
+          half = fmaxf(half, y(u, i));
+          if (!kUni) up2 = fmaxf(up2, y(u, i) + ve[u][kUni ? 0 : i]);
         }
         up = fmaxf(up, half);
-        if (kUni)
-          up2 = fmaxf(up2, half + ve[u][0]);
+        if (kUni) up2 = fmaxf(up2, half + ve[u][0]);
       }
       if (a.scores != nullptr && (NT == 2 || gid < 4) && head_ok) {
         float* const o = a.scores + (unit * a.G + head) * a.score_stride + cur.ls * kStep +
                          warp * kTile + 2 * q;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          float y[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = there(u, i) ? x[u][i] * sf[u][kUni ? 0 : i] : -INFINITY;
-          *reinterpret_cast<float2*>(o + 16 * u) = make_float2(y[0], y[1]);
-          *reinterpret_cast<float2*>(o + 16 * u + 8) = make_float2(y[2], y[3]);
+          *reinterpret_cast<float2*>(o + 16 * u) = make_float2(y(u, 0), y(u, 1));
+          *reinterpret_cast<float2*>(o + 16 * u + 8) = make_float2(y(u, 2), y(u, 3));
         }
       }
-      up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 1));
-      up2 = fmaxf(up2, __shfl_xor_sync(0xffffffffu, up2, 1));
-      up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, 2));
-      up2 = fmaxf(up2, __shfl_xor_sync(0xffffffffu, up2, 2));
-      if (__any_sync(0xffffffffu, up > m || up2 > m2)) {
-        const float mn = fmaxf(m, ceilf(up)), m2n = fmaxf(m2, ceilf(up2));
-        l *= ref_change(m, mn);
-        const float r = ref_change(m2, m2n);
-        const float f0 = __shfl_sync(0xffffffffu, r, 8 * q);       // column 2 q
-        const float f1 = __shfl_sync(0xffffffffu, r, 8 * q + 4);   // column 2 q + 1
+      if (__any_sync(0xffffffffu, up > m || up2 > m + r || big)) {
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+          up = fmaxf(up, __shfl_xor_sync(0xffffffffu, up, o));
+          up2 = fmaxf(up2, __shfl_xor_sync(0xffffffffu, up2, o));
+        }
+        const float mn = fmaxf(m, ceilf(up)), step = ref_step(m, mn);
+        up2 -= mn;
+        // Scores of 256 and more are rounded before m is subtracted, and ve is added to the
+        // difference: fp32 cannot place m within 1 of an exact x of 2^24 and more, nor add ve to
+        // it; and the sums kernel, which gets rounded scores, forms the same weights.
+        big = big || (fabsf(mn) >= 256.0f && mn != -INFINITY);
+        if (__any_sync(0xffffffffu, big)) {
+          float rt = -INFINITY;
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              rt = fmaxf(rt, (y(u, i) - mn) + ve[u][kUni ? 0 : i]);
+              if (big) x[u][i] *= sf[u][kUni ? 0 : i];
+            }
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < kSc; ++i) sf[u][i] = big ? 1.0f : sf[u][i];
+          rt = fmaxf(rt, __shfl_xor_sync(0xffffffffu, rt, 1));
+          up2 = fmaxf(rt, __shfl_xor_sync(0xffffffffu, rt, 2));
+        }
+        const float rn = fmaxf(r + step, ceilf(up2));
+        m = mn;
+        l *= ex2(step);
+        const float f = ref_change(r + step, rn);
+        r = rn;
+        const float f0 = __shfl_sync(0xffffffffu, f, 8 * q);       // column 2 q
+        const float f1 = __shfl_sync(0xffffffffu, f, 8 * q + 4);   // column 2 q + 1
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
           acc[t][0] *= f0;
@@ -844,13 +880,10 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
           acc[t][2] *= f0;
           acc[t][3] *= f1;
         }
-        m = mn;
-        m2 = m2n;
       }
-      // w = 2^(x + E - m2 + 14) (c / 2^E), E = ve - 1: formed by itself, since p and 2^(m - m2) c can
-      // each leave the range of fp32 where w does not (a block of zeros may lead by 100 and more,
-      // and m2 then lies as far below m).  c / 2^E is c's mantissa, but for scales below 2^-126 (and 0).
-      const float ref_w = (kWBias - 1.0f) - m2;
+      // w = 2^(d + E - r) (c / 2^E) 2^14, d = x - m, E = ve - 1: formed by itself, since p = 2^d and 2^-r c can each
+      // leave the range of fp32 where w does not (a block of zeros may lead by 100 and more,
+      // and r then lies as low).  c / 2^E is c's mantissa, but for scales below 2^-126 (and 0).
       uint32_t b[2][NT][2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -858,16 +891,16 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
 #pragma unroll
         for (int i = 0; i < kSc; ++i) {
           const uint32_t bits = __float_as_uint(vsc[u][i]);
-          up_w[i] = ve[u][i] + ref_w;
-          mant[i] = bits < 0x800000u ? vsc[u][i] * 0x1p127f
-                                     : __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+          up_w[i] = ve[u][i] + (-1.0f - r);
+          mant[i] = bits < 0x800000u ? vsc[u][i] * 0x1p126f * 0x1p15f
+                                     : __uint_as_float((bits & 0x7fffffu) | 0x46800000u);
         }
         float w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float y = x[u][i], f = sf[u][kUni ? 0 : i];
-          l += there(u, i) ? ex2(fmaf(y, f, -m)) : 0.0f;
-          w[i] = there(u, i) ? ex2(fmaf(y, f, up_w[kUni ? 0 : i])) * mant[kUni ? 0 : i] : 0.0f;
+        for (int i = 0; i < 4; ++i) {   // a key that is not there has d = -inf, and p = w = 0
+          const float d = there(u, i) ? fmaf(x[u][i], sf[u][kUni ? 0 : i], -m) : -INFINITY;
+          l += ex2(d);
+          w[i] = ex2(d + up_w[kUni ? 0 : i]) * mant[kUni ? 0 : i];
         }
         b[u][0][0] = pack_f16(w[0], w[1]);
         b[u][0][1] = pack_f16(w[2], w[3]);
@@ -964,7 +997,7 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
       if (q == 0 && (NT == 2 || gid < 4)) {
         sm.stat[warp][head][0] = m;
         sm.stat[warp][head][1] = l;
-        sm.stat[warp][head][2] = m2;
+        sm.stat[warp][head][2] = r;
       }
       // High and low parts together.  NT = 1: lanes q and q ^ 2 hold the two parts of two
       // heads; each keeps half of the dimensions (value 4 t + i: tile t + 4 (q / 2)).
@@ -995,26 +1028,27 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
       // dimension 16 gid (+ 8 (q / 2)) + v / 2; thread (head, 4 dimensions) sums the warps
       for (int i = tid; i < a.G * (kD / 4); i += kThr) {
         const int hh = i / (kD / 4), d = 4 * (i % (kD / 4));
-        float hM = -INFINITY, hM2 = -INFINITY, hl = 0.0f;
+        float hM = -INFINITY, hR = -INFINITY, hl = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          hM = fmaxf(hM, sm.stat[w][hh][0]);
-          hM2 = fmaxf(hM2, sm.stat[w][hh][2]);
-        }
+        for (int w = 0; w < kWarps; ++w) hM = fmaxf(hM, sm.stat[w][hh][0]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+          hR = fmaxf(hR, sm.stat[w][hh][2] + ref_step(sm.stat[w][hh][0], hM));
         const int ln = 4 * (d >> 4) + (NT == 1 ? (hh >> 1) + 2 * ((d >> 3) & 1) : hh >> 1);
         const int v0 = 2 * (NT == 1 ? d & 7 : d & 15) + (hh & 1);
         float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          hl += sm.stat[w][hh][1] * ref_change(sm.stat[w][hh][0], hM);
-          const float f = ref_change(sm.stat[w][hh][2], hM2);
+          const float step = ref_step(sm.stat[w][hh][0], hM);
+          hl += sm.stat[w][hh][1] * ex2(step);
+          const float f = ref_change(sm.stat[w][hh][2] + step, hR);
 #pragma unroll
           for (int e = 0; e < 4; ++e) t[e] = fmaf(sm.sums[w][v0 + 2 * e][ln], f, t[e]);
         }
         if (parts == 1) {
           const bool some = hl > 0.0f || !(hl == hl);   // an empty list: zeros
           *reinterpret_cast<float4*>(a.out + (unit * a.G + hh) * kD + d) =
-              OutScale(hM, hM2, hl, some).of(t[0], t[1], t[2], t[3]);
+              OutScale(hR, hl, some).of(t[0], t[1], t[2], t[3]);
           if (d == 0 && a.stats != nullptr) {
             float* const o = a.stats + (unit * a.G + hh) * 2;
             o[0] = some ? hM : 0.0f;
@@ -1024,7 +1058,7 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
           *reinterpret_cast<float4*>(slot + hh * kPart + 4 + d) =
               make_float4(t[0], t[1], t[2], t[3]);
           if (d == 0)
-            *reinterpret_cast<float4*>(slot + hh * kPart) = make_float4(hM, hl, hM2, 0.0f);
+            *reinterpret_cast<float4*>(slot + hh * kPart) = make_float4(hM, hl, hR, 0.0f);
         }
       }
       __syncthreads();   // the part is written; sums and stat are free again
