@@ -540,7 +540,7 @@ adamas_status adamas_kv8_append(const adamas_kv8_cache* cache, const void* k_new
                                 cudaStream_t stream);
 
 /*
- * Values of the n positions from starts[b] (device int32 [B]) of every sequence and kv
+ * Values of the n positions (1 <= n <= 2^30) from starts[b] (device int32 [B]) of every sequence and kv
  * head: k_out, v_out [B][Hkv][n][d] elements of out_dt, v * S rounded to out_dt (bf16:
  * exact for power-of-two scales).  Positions outside [0, Lmax) give zeros.
  */

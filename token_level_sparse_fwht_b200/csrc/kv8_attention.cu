@@ -50,9 +50,12 @@
 // whole tile's time more to arrive, and a row's address is formed once instead of by every lane
 // that holds a piece of it (8 sequences x 32 lists of 1024 keys: 22 us; straight into registers 25.6).
 //
-// Measured, e4m3 and bf16 queries: 32 kv heads x 128K keys 182 us, 6.1 TB/s of the 6.55 that a copy
-// reaches; 8 kv heads x 32K keys, 4 query heads each, 19.4 us (3.5 TB/s: about 8 us go to the
-// launches, the first loads and the merges, which 1000 keys take as well: 7.9 us).
+// Measured, e4m3 and bf16 queries: 32 kv heads x 128K keys 187 us in single passes (1.074 GB, 5.7
+// TB/s of the 6.55 that a copy reaches), 197 with running sums (1.108 GB); call after call, when the
+// card sits at its power limit, 206 to 214 with sums.  8 kv heads x 32K keys, 4 query heads each,
+// 19.5 us (3.4 TB/s: about 8 us go to the launches, the first loads and the merges, which 1000 keys take
+// as well: 8.2 us).  Of the register-path variants the one for bf16 queries, e4m3 and G <= 4 spills
+// nothing, the others 12 to 72 bytes; the ring variants nothing.
 #include <type_traits>
 
 #include "kv8_internal.cuh"
@@ -378,10 +381,11 @@ __host__ __device__ inline int whole_units(int units, int steps_per_unit, int gr
 // Merges the parts (in CTA order) of the units that were cut; block c looks at what CTA c left.  A
 // unit of at most kFewParts parts is merged by the block of its first CTA, a warp per head; of one in more
 // (so cut into at least a first, 7 inner and a last part) the block of part h takes head h, thread p
-// finding part p's factor before warp w sums parts w, w + 8, ..., 4 dimensions per lane.  So one
-// long sequence among many short ones is not left to a warp.  (The launch bound of 2 blocks is for the
-// 80 registers that hold a warp's 8 parts at once; left to itself the compiler took 64, and two rounds.)  (With blocks for all heads of every CTA
-// one sequence of 1000 keys took 8.4 us and one of 32K 19.6, so 7.9 and 19.4.)
+// finding part p's reference before warp w sums parts w, w + 8, ..., 4 dimensions per lane.  So one
+// long sequence among many short ones is not left to a warp.  (With blocks for all heads of every CTA
+// one sequence of 1000 keys took 0.5 us more and one of 32K 0.2.)  The launch bound of 2 blocks is for
+// the 80 registers that hold a warp's 8 parts at once: left to itself the compiler took 64 and two
+// rounds of loads, 6.3 us instead of 5.6 by itself.
 constexpr int kCombineThreads = 256, kFewParts = 8;
 
 __global__ void __launch_bounds__(kCombineThreads, 2) kv8_combine_kernel(
@@ -451,7 +455,7 @@ __global__ void __launch_bounds__(kCombineThreads, 2) kv8_combine_kernel(
       if (p < parts) y[u] = __ldcg(at(p) + 1 + lane);
     }
   };
-  load(warp);   // under way while the factors are found
+  load(warp);   // under way while the references are found
   constexpr int kSt = (kMaxParts + kCombineThreads - 1) / kCombineThreads;
   float M = -INFINITY, R = -INFINITY;
   float4 st[kSt];
@@ -881,9 +885,10 @@ __global__ void __launch_bounds__(kThr, kCtasPerSm) kv8_attention_kernel(const A
           acc[t][3] *= f1;
         }
       }
-      // w = 2^(d + E - r) (c / 2^E) 2^14, d = x - m, E = ve - 1: formed by itself, since p = 2^d and 2^-r c can each
-      // leave the range of fp32 where w does not (a block of zeros may lead by 100 and more,
-      // and r then lies as low).  c / 2^E is c's mantissa, but for scales below 2^-126 (and 0).
+      // w = 2^(d + E - r) (c / 2^E) 2^14, d = x - m, E = ve - 1: formed by itself, since p = 2^d and
+      // 2^-r c can each leave the range of fp32 where w does not (a block of zeros may lead by
+      // 100 and more, and r then lies as low).  c / 2^E is c's mantissa, but for scales below
+      // 2^-126 (and 0).
       uint32_t b[2][NT][2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -1101,8 +1106,8 @@ __global__ void __launch_bounds__(256) kv8_weights_kernel(
     s[u] = 0.0f;
   }
   // kHeads heads' scores at once (G = 1: 1, G <= 4: 4, else 8), so that their latencies overlap: 17
-  // ragged sequences with 8 heads to a kv head take 33.6 us in all, 34.9 one by one; 32K with 4 heads
-  // 23.2 against 23.7.
+  // ragged sequences with 8 heads to a kv head take 1.3 us less in all than one by one (of 32), 32K with
+  // 4 heads 0.5 (of 23).
   for (int g0 = 0; g0 < G; g0 += kHeads) {
     float x[kHeads][kWPer], M[kHeads], inv[kHeads];
 #pragma unroll

@@ -19,8 +19,8 @@ namespace cg = cooperative_groups;
 // counts what it keeps, learns its offset from its peers, and writes positions and weights
 // in order.  Protected positions (first `sink`, last `recent`) are kept besides.
 // The chain of three steps bounds it (histogram in shared memory, cluster barrier, search of the
-// bins): 8 units of 32K weights take 14 us; 128 units of up to 16K 33 us, bound by the instructions
-// of the three passes.
+// bins): 8 units of 32K weights take 14 us.  128 units of up to 16K take 33 us: they get two CTAs
+// each, and as a CTA's 1024 threads take an SM, 256 CTAs on 148 SMs are two waves.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
@@ -242,7 +242,9 @@ constexpr int kMoveThreads = 512;
 // A thread holds a quarter of a row (32 bytes; what is done per row, its address, scale and ratio,
 // is then done four times, not eight as with 16 bytes: 133 -> 115 us when it was taken,
 // for 16 x 8 units cut from 16K to 6K rows).
-// Rows per thread: in place every round costs a cluster barrier, so it takes more rows.  Into
+// Rows per thread: in place every round costs a cluster barrier, so it takes more rows (at 128
+// registers about 90 bytes of the next round's rows are spilled; 8 units cut from 32K to 8K rows take 44 us with
+// the selection, into another cache 28, caches flushed).  Into
 // another cache a CTA is as small as a block allows (at least 64 rows), so that few warps wait at
 // its barrier; before the runs, one row per thread took 131 us instead of 103 (the whole call), four
 // 124.  Bound by the dependent loads at up to 32 warps per SM: what is moved there, 321 MB, would take
