@@ -488,7 +488,8 @@ adamas_status adamas_decode_plan_shared(int B, int Hq, int Hkv, int d, int64_t L
  * page block_table[b * max_blocks_per_seq + p / page_size], and Lmax is the longest
  * sequence (Lmax <= max_blocks_per_seq * page_size).  block_size is a power of two in
  * [1, 256]; contiguous caches need Lmax % block_size == 0.  A cache has at most 2^31 - 1 rows
- * (B * Hkv * Lmax, or num_pages * Hkv * page_size; ADAMAS_ERR_UNSUPPORTED above).  A page that is written
+ * (B * Hkv * Lmax, or num_pages * Hkv * page_size), 2^24 units (B * Hkv) and 2^30
+ * positions in a sequence (ADAMAS_ERR_UNSUPPORTED above).  A page that is written
  * (append, evict) must belong to one sequence.  codes may be NULL.  Alignment: 16
  * bytes for rows and codes, 4 for scales and integer arrays, 256 for workspaces.
  *

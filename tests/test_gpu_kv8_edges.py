@@ -429,3 +429,40 @@ def test_append_codes_of_every_form(dtype, fmt, block, kw):
         rest = np.ones(c.cap, bool)
         rest[starts[b]:starts[b] + counts[b]] = False
         assert np.array_equal(codes[b][:, rest], c.codes[b][:, rest])
+
+
+def test_evict_of_more_sums_than_32_bits_count():
+    """1024 sequences x 16 kv heads x 131072 positions are 2^31 running sums, although the sequences here
+    are short and hold a page each: the cache's own rows are few."""
+    B, H, page, L, budget = 1024, 16, 64, 131072, 24
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randint(0, 256, (B, H, page, D), generator=g, device="cuda", dtype=torch.uint8)
+            .view(torch.int8).clamp(-127, 127) for _ in range(2))
+    ks, vs = (torch.exp2(torch.randint(-6, 6, (B, H, page // 16), generator=g, device="cuda").float())
+              for _ in range(2))
+    table = torch.randperm(B, generator=g, device="cuda").int()[:, None].expand(-1, L // page).contiguous()
+    cache, ws = ad.KV8Cache(k, v, ks, vs, 16, block_table=table), ad.kv8_workspace()
+    assert cache.Lmax == L
+    old = ad.kv8_read(cache, 0, page, ws, dtype=torch.float32)
+    w = torch.zeros((B, H, L), device="cuda")
+    sums = torch.rand((B, H, page), generator=g, device="cuda")
+    w[..., :page] = sums
+    lens = torch.randint(0, page + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    lens[-1] = page
+    was = lens.tolist()
+    keep, _ = ad.kv8_evict(cache, w, lens, budget, ws, sink=2, recent=5)
+    ad.check_workspace(ws)
+    new = ad.kv8_read(cache, 0, budget, ws, dtype=torch.float32)
+    for b in (0, 1, 511, 700, B - 1):
+        for h in (0, H - 1):
+            want = ref.evict_select(sums[b, h].cpu().numpy(), was[b], budget, 2, 5)
+            n = len(want)
+            assert np.array_equal(keep[b, h, :n].cpu().numpy(), want) and lens[b].item() == n
+            assert torch.equal(w[b, h, :n], sums[b, h, want]) and not w[b, h, n:was[b]].any()
+            assert torch.equal(w[b, h, was[b]:page], sums[b, h, was[b]:])   # behind a sequence: left
+            for x, y in zip(new, old):
+                stored, scale = ref.requantise(y[b, h, want].double().cpu().numpy(), "int8", 16)
+                if was[b] > budget:
+                    assert np.array_equal(x[b, h, :n].double().cpu().numpy(), stored * scale.repeat(16)[:n, None])
+                else:
+                    assert torch.equal(x[b, h, :n], y[b, h, :n])

@@ -264,10 +264,10 @@ adamas_status adamas_evict_select(const float* weights, int B, int Hkv, int64_t 
                                   const int32_t* seq_lens, int budget, int sink, int recent,
                                   int32_t* keep, float* weights_out, int64_t Lmax_out,
                                   void* workspace, size_t ws_bytes, cudaStream_t stream) {
-  if (!weights || !seq_lens || !keep) return ADAMAS_ERR_INVALID_ARG;
-  Kv8 c{};
-  const adamas_status s = check_layout(B, Hkv, Lmax, 0, 0, nullptr, 0, c);
-  if (s != ADAMAS_OK) return s;
+  if (!weights || !seq_lens || !keep || B <= 0 || Hkv <= 0 || Lmax <= 0)
+    return ADAMAS_ERR_INVALID_ARG;
+  // weights are indexed with 64 bits: no limit on B * Hkv * Lmax
+  if (int64_t(B) * Hkv > (1 << 24) || Lmax > kMaxLen) return ADAMAS_ERR_UNSUPPORTED;
   if (budget <= 0 || sink < 0 || recent < 0 || int64_t(sink) + recent > budget ||
       int64_t(budget) > kMaxLen)
     return ADAMAS_ERR_INVALID_ARG;
